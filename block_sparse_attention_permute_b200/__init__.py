@@ -18,7 +18,7 @@ import os
 
 import torch
 
-__all__ = ["Plan", "BsaError", "TOPK", "TOPP", "lib_path", "load"]
+__all__ = ["Plan", "Rope", "BsaError", "TOPK", "TOPP", "lib_path", "load"]
 
 TOPK = 0
 TOPP = 1
@@ -93,6 +93,9 @@ def load():
         "bsa_attention_paired": [P, P, P, P, P, P, I, P, Z, P, P, P],
         "bsa_forward_grouped": [P, I, P, P, P, P, I, P, P, P, P, P, P, P, Z, P, P],
         "bsa_aggregation_scores": [P, I, P, P, P, P, P],
+        "bsa_rope_create": [ctypes.POINTER(P), P, ctypes.POINTER(RopeConfig)],
+        "bsa_rope_destroy": [P],
+        "bsa_rotary": [P, P, P, P, P, P, I, P],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -149,6 +152,42 @@ def mask_union(heads, window=(-1, -1), sink_tokens=0, intra_mode=0, intra_params
         u._keep = arr
         u.intra_param = ctypes.cast(arr, ctypes.POINTER(ctypes.c_double))
     return u
+
+
+class RopeConfig(ctypes.Structure):
+    """bsa_rope_config_t (axes in the order t, y, x)."""
+    _fields_ = [("dim", ctypes.c_int * 3), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double * 3),
+                ("orig_len", ctypes.c_double * 3), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("mscale", ctypes.c_double),
+                ("heads_k", ctypes.c_int)]
+
+
+_ROPE_LAYOUT = {"interleaved": 0, "half": 1}
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _check_view(t, shape, dtype, device, name):
+    """A strided tensor (bsa_view_t): its head dimension contiguous, the rest checked by the call."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise BsaError(1, f"{name} must be a tensor on {device}")
+    if t.dtype != dtype or t.shape != shape or t.stride(3) != 1:
+        raise BsaError(1, f"{name} must be a {dtype} tensor of shape {tuple(shape)} whose last axis is "
+                          f"contiguous, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _views(*tensors):
+    """One bsa_view_t per tensor (None: zeros) and their addresses (None: NULL)."""
+    flat = []
+    for t in tensors:
+        flat += (0, 0, 0, 0) if t is None else (t.data_ptr(), *t.stride()[:3])
+    arr = (ctypes.c_longlong * len(flat))(*flat)
+    base = ctypes.addressof(arr)
+    return arr, [None if t is None else base + 32 * i for i, t in enumerate(tensors)]
+
+
+def _triple(x, kind=float):
+    return (kind(x),) * 3 if isinstance(x, (int, float)) else tuple(kind(v) for v in x)
 
 
 class Plan:
@@ -366,6 +405,16 @@ class Plan:
                                         ctypes.byref(t)))
         return out, t.as_dict()
 
+    # ------------------------------------------------------ rotary positions
+    def rope(self, dims, theta=10000.0, layout="interleaved", scaling="none", factor=1.0,
+             orig_len=None, beta_fast=32.0, beta_slow=1.0, mscale=1.0, heads_k=None) -> "Rope":
+        """Rotary positions over this plan's grid (bsa_rope_create): dims = rotated elements of
+        the t, y and x axis; layout "interleaved" or "half"; scaling "none", "linear", "ntk" or
+        "yarn" by factor (one number or one per axis; "yarn" also takes the trained orig_len);
+        heads_k = heads of K where it has fewer than Q."""
+        return Rope(self, dims, theta, layout, scaling, factor, orig_len, beta_fast, beta_slow,
+                    mscale, heads_k)
+
     # --------------------------------------------------------- mask union
     def kmax_for_union(self, mode, params, union) -> int:
         k = ctypes.c_int()
@@ -476,6 +525,68 @@ class Plan:
         """Bound of the attention kernel's in-kernel waits (0 = default, about a
         second) and the timeout path's test hook (bsa_plan_set_watchdog)."""
         _check(load().bsa_plan_set_watchdog(self._h, int(wait_limit_cycles), int(withhold_copy)))
+
+
+class Rope:
+    """Rotary positions of one plan's tokens; made by Plan.rope."""
+
+    def __init__(self, plan, dims, theta, layout, scaling, factor, orig_len, beta_fast, beta_slow,
+                 mscale, heads_k):
+        if layout not in _ROPE_LAYOUT or scaling not in _ROPE_SCALING:
+            raise BsaError(1, f"unknown rope layout {layout!r} or scaling {scaling!r}")
+        dims, factor, orig_len = _triple(dims, int), _triple(factor), _triple(orig_len or 0.0)
+        if not (len(dims) == len(factor) == len(orig_len) == 3):
+            raise BsaError(1, "dims, factor and orig_len take one value or one per axis (t, y, x)")
+        i = plan.info
+        c = RopeConfig((ctypes.c_int * 3)(*dims), _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling],
+                       float(theta), (ctypes.c_double * 3)(*factor), (ctypes.c_double * 3)(*orig_len),
+                       float(beta_fast), float(beta_slow), float(mscale), int(heads_k or 0))
+        self.device, self.dtype = plan.device, plan.dtype
+        self.q_shape = torch.Size(plan.orig_shape)
+        self.k_shape = torch.Size((i.batch, i.n_tot, heads_k or i.heads, i.head_dim))
+        self._h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(load().bsa_rope_create(ctypes.byref(self._h), plan._h, ctypes.byref(c)))
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h and _lib is not None:
+            _lib.bsa_rope_destroy(h)
+            self._h = None
+
+    def apply(self, q, k=None, t_origin=None, out=None):
+        """Rotates q [B,Ntot,heads,D] and k [B,Ntot,heads_k,D] (strided views are fine).
+
+        t_origin: int64 [B], added to t.  out: (q_out, k_out), or one tensor without k; the
+        inputs themselves for a rotation in place.  Returns (q_out, k_out), or q_out without k."""
+        return self._run(q, k, t_origin, out, 0)
+
+    def backward(self, dq, dk=None, t_origin=None, out=None):
+        """The gradients of apply's inputs from those of its outputs (the transposed rotation)."""
+        return self._run(dq, dk, t_origin, out, 1)
+
+    def _run(self, q, k, t_origin, out, backward):
+        dev, dt = self.device, self.dtype
+        _check_view(q, self.q_shape, dt, dev, "q")
+        if k is not None:
+            _check_view(k, self.k_shape, dt, dev, "k")
+        if t_origin is not None and (t_origin.dtype != torch.int64 or t_origin.device != dev or
+                                     t_origin.shape != self.q_shape[:1] or
+                                     not t_origin.is_contiguous()):
+            raise BsaError(1, f"t_origin must be an int64 tensor of shape {tuple(self.q_shape[:1])} on {dev}")
+        if out is None:
+            qo = torch.empty(self.q_shape, dtype=dt, device=dev)
+            ko = None if k is None else torch.empty(self.k_shape, dtype=dt, device=dev)
+        else:
+            qo, ko = out if k is not None else (out, None)
+            _check_view(qo, self.q_shape, dt, dev, "q_out")
+            if k is not None:
+                _check_view(ko, self.k_shape, dt, dev, "k_out")
+        keep, v = _views(q, k, qo, ko)
+        with torch.cuda.device(dev):
+            _check(load().bsa_rotary(self._h, *v, None if t_origin is None else t_origin.data_ptr(),
+                                     backward, _stream(dev)))
+        return qo if k is None else (qo, ko)
 
 
 def aggregation_scores(plans, x):

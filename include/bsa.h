@@ -495,6 +495,84 @@ bsa_status bsa_attention_paired(bsa_plan_t plan, const void* q, const void* k,
                                 size_t ws_bytes, void* o, int32_t* dev_status,
                                 void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions and cross attention (no counterpart on the pages: the steps
+ * of a video DiT block on either side of the block-sparse self-attention).
+ * Their tensors are views, so that the parts of a fused projection can be
+ * passed without a copy. */
+
+/* A tensor [B, N, heads, head_dim] in device memory: element (b, n, h, d) is
+ * at ptr[b * batch + n * token + h * head + d] (strides in elements, the head
+ * dimension contiguous).  ptr and, for axes longer than 1, the strides must be
+ * multiples of 16 bytes and not negative; an input's stride may be 0 (the same
+ * values along that axis), an output's elements must not overlap. */
+typedef struct {
+  void* ptr;
+  long long batch, token, head;
+} bsa_view_t;
+
+/* Which elements of a head form pair p of the R / 2 rotated pairs. */
+typedef enum {
+  BSA_ROPE_INTERLEAVED = 0, /* (2p, 2p + 1)  */
+  BSA_ROPE_HALF = 1         /* (p, p + R/2)  */
+} bsa_rope_layout;
+
+/* How the pairs' frequencies f = theta^(-2i/d) (pair i of an axis of d
+ * elements) are changed for grids longer than trained on, s = factor:
+ *  LINEAR  f / s (position interpolation);
+ *  NTK     theta -> theta * s^(d / (d - 2)) (d = 2: unchanged), which keeps the
+ *          fastest pair and divides the slowest by s;
+ *  YARN    (1 - g) f / s + g f with g the clamped ramp from 0 at beta_slow to 1
+ *          at beta_fast turns within orig_len positions, orig_len f / (2 pi). */
+typedef enum {
+  BSA_ROPE_NONE = 0,
+  BSA_ROPE_LINEAR = 1,
+  BSA_ROPE_NTK = 2,
+  BSA_ROPE_YARN = 3
+} bsa_rope_scaling;
+
+/* Axes are in the order t, y, x. */
+typedef struct {
+  int dim[3];              /* rotated elements per axis: even, >= 0; their sum R
+                              is in [2, head_dim]; the head's elements past R
+                              are passed through                              */
+  bsa_rope_layout layout;
+  bsa_rope_scaling scaling;
+  double theta;            /* > 1                                             */
+  double factor[3];        /* >= 1 (read unless scaling is BSA_ROPE_NONE)     */
+  double orig_len[3];      /* > 0 (BSA_ROPE_YARN)                             */
+  double beta_fast, beta_slow; /* beta_fast > beta_slow >= 0 (BSA_ROPE_YARN)  */
+  double mscale;           /* > 0: multiplies every rotated element           */
+  int heads_k;             /* heads of K; 0 = the plan's                      */
+} bsa_rope_config_t;
+
+typedef struct bsa_rope_s* bsa_rope_t;
+
+/* bsa_rope_create — rotary positions over a plan's latent grid: video token
+ * (t, y, x) turns the pairs of the t, y and x axis by t f, y f and x f (pairs
+ * in the order of the axes); text tokens are passed through.  The plan is
+ * copied from, not kept.  The object holds no device memory.
+ * bsa_rope_destroy frees it. */
+bsa_status bsa_rope_create(bsa_rope_t* out, bsa_plan_t plan,
+                           const bsa_rope_config_t* config);
+bsa_status bsa_rope_destroy(bsa_rope_t rope);
+
+/* bsa_rotary — rotates Q and K (plan dtype) in one launch:
+ *   (a, b) -> mscale (a cos - b sin, a sin + b cos) for every pair,
+ * the angles reduced in double, the products in fp32, rounded once.
+ *   q, q_out   [B, Ntot, heads, D] views
+ *   k, k_out   [B, Ntot, heads_k, D] views (both NULL = Q alone)
+ *   t_origin   device int64 [B] or NULL: added to t in each batch element (how
+ *              far into its sequence it is); |t_origin + t| < 2^52
+ *   backward   0, or 1 for the transposed map: from gradients of the outputs
+ *              to gradients of the inputs
+ * An output may be the same view as its input (in place; the parts that are
+ * passed through are then not touched); any other overlap between the views
+ * is not allowed.  Captures into a CUDA graph; t_origin is read by the kernel. */
+bsa_status bsa_rotary(bsa_rope_t rope, const bsa_view_t* q, const bsa_view_t* k,
+                      const bsa_view_t* q_out, const bsa_view_t* k_out,
+                      const int64_t* t_origin, int backward, void* stream);
+
 /* bsa_check_status — synchronise `stream`, read and clear the plan-owned
  * status word; returns BSA_OK or the recorded error. */
 bsa_status bsa_check_status(bsa_plan_t plan, void* stream);
