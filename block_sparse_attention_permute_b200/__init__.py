@@ -18,7 +18,7 @@ import os
 
 import torch
 
-__all__ = ["Plan", "Rope", "BsaError", "TOPK", "TOPP", "lib_path", "load"]
+__all__ = ["Plan", "Rope", "CrossAttention", "BsaError", "TOPK", "TOPP", "lib_path", "load"]
 
 TOPK = 0
 TOPP = 1
@@ -96,6 +96,12 @@ def load():
         "bsa_rope_create": [ctypes.POINTER(P), P, ctypes.POINTER(RopeConfig)],
         "bsa_rope_destroy": [P],
         "bsa_rotary": [P, P, P, P, P, P, I, P],
+        "bsa_cross_create": [ctypes.POINTER(P)] + [I] * 7 + [ctypes.c_double],
+        "bsa_cross_destroy": [P],
+        "bsa_cross_workspace_size": [P, ctypes.POINTER(Z), ctypes.POINTER(Z)],
+        "bsa_cross_attention": [P] * 9 + [Z, P, P],
+        "bsa_cross_attention_backward": [P] * 13 + [Z, P, P],
+        "bsa_cross_check_status": [P, P],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -415,6 +421,12 @@ class Plan:
         return Rope(self, dims, theta, layout, scaling, factor, orig_len, beta_fast, beta_slow,
                     mscale, heads_k)
 
+    def cross(self, n_kv, heads_kv=None, scale=None) -> "CrossAttention":
+        """Cross attention from this plan's tokens (video, then text) to n_kv encoder states."""
+        i = self.info
+        return CrossAttention(i.batch, i.n_tot, n_kv, i.heads, heads_kv, i.head_dim, self.dtype,
+                              scale, self.device)
+
     # --------------------------------------------------------- mask union
     def kmax_for_union(self, mode, params, union) -> int:
         k = ctypes.c_int()
@@ -587,6 +599,122 @@ class Rope:
             _check(load().bsa_rotary(self._h, *v, None if t_origin is None else t_origin.data_ptr(),
                                      backward, _stream(dev)))
         return qo if k is None else (qo, ko)
+
+
+class CrossAttention:
+    """Cross attention from n_q query tokens to n_kv encoder states (bsa_cross_create).
+
+    q, o [B,n_q,heads,D]; k, v [B,n_kv,heads_kv,D] (strided views are fine).  kv_len: int32 [B],
+    keys of each batch element; key_mask: bool or uint8 [B,n_kv], False at padding."""
+
+    def __init__(self, batch, n_q, n_kv, heads, heads_kv=None, head_dim=128, dtype=torch.bfloat16,
+                 scale=None, device=None):
+        L = load()
+        if dtype not in _DT:
+            raise BsaError(1, f"dtype must be float32 or bfloat16, got {dtype}")
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
+            else torch.device(device)
+        if self.device.type != "cuda":
+            raise BsaError(1, "libbsa runs on CUDA devices only")
+        if scale is not None and not scale > 0.0:
+            raise BsaError(1, f"scale must be above 0, got {scale}")
+        heads_kv = heads if heads_kv is None else heads_kv
+        self.dtype = dtype
+        self._h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(L.bsa_cross_create(ctypes.byref(self._h), batch, n_q, n_kv, heads, heads_kv,
+                                      head_dim, _DT[dtype], float(scale or 0.0)))
+        self.q_shape = torch.Size((batch, n_q, heads, head_dim))
+        self.kv_shape = torch.Size((batch, n_kv, heads_kv, head_dim))
+        self.lse_shape = torch.Size((batch, heads, n_q))
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(L.bsa_cross_workspace_size(self._h, ctypes.byref(f), ctypes.byref(b)))
+        self.forward_ws, self.backward_ws = f.value, b.value
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h and _lib is not None:
+            try:
+                with torch.cuda.device(self.device):
+                    _lib.bsa_cross_destroy(h)
+            except Exception:
+                pass
+            self._h = None
+
+    def _view(self, t, kv, name):
+        _check_view(t, self.kv_shape if kv else self.q_shape, self.dtype, self.device, name)
+
+    def _masks(self, kv_len, key_mask):
+        for t, shape, types, name in ((kv_len, self.kv_shape[:1], (torch.int32,), "kv_len"),
+                                      (key_mask, self.kv_shape[:2], (torch.bool, torch.uint8), "key_mask")):
+            if t is not None and (t.device != self.device or t.dtype not in types or
+                                  t.shape != shape or not t.is_contiguous()):
+                raise BsaError(1, f"{name} must be a contiguous {types[0]} tensor of shape "
+                                  f"{tuple(shape)} on {self.device}")
+        return (None if kv_len is None else kv_len.data_ptr(),
+                None if key_mask is None else key_mask.data_ptr())
+
+    def _workspace(self, ws, need):
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size()), ws
+
+    def _lse(self, lse):
+        if not isinstance(lse, torch.Tensor) or lse.device != self.device or \
+                lse.dtype != torch.float32 or lse.shape != self.lse_shape or not lse.is_contiguous():
+            raise BsaError(1, f"lse must be a contiguous float32 tensor of shape {tuple(self.lse_shape)} "
+                              f"on {self.device}")
+
+    def forward(self, q, k, v, kv_len=None, key_mask=None, out=None, return_lse=False,
+                workspace=None, dev_status=None):
+        """O = softmax(scale Q K^T) V; with return_lse also the log-sum-exp of every row
+        (float32 [B,heads,n_q]), which backward takes."""
+        self._view(q, False, "q")
+        self._view(k, True, "k")
+        self._view(v, True, "v")
+        if out is None:
+            out = torch.empty(self.q_shape, dtype=self.dtype, device=self.device)
+        else:
+            self._view(out, False, "o")
+        lse = torch.empty(self.lse_shape, dtype=torch.float32, device=self.device) if return_lse else None
+        keep, views = _views(q, k, v, out)
+        masks = self._masks(kv_len, key_mask)
+        ws, keep_ws = self._workspace(workspace, self.forward_ws)
+        with torch.cuda.device(self.device):
+            _check(load().bsa_cross_attention(self._h, *views[:3], *masks, views[3],
+                                              None if lse is None else lse.data_ptr(), *ws,
+                                              None if dev_status is None else dev_status.data_ptr(),
+                                              _stream(self.device)))
+        return (out, lse) if return_lse else out
+
+    def backward(self, d_o, q, k, v, o, lse, kv_len=None, key_mask=None, out=None, workspace=None,
+                 dev_status=None):
+        """(dq, dk, dv) from d_o, the forward's inputs and its outputs o and lse; out: the three
+        tensors to write."""
+        for t, kv, name in ((d_o, False, "d_o"), (q, False, "q"), (k, True, "k"), (v, True, "v"),
+                            (o, False, "o")):
+            self._view(t, kv, name)
+        self._lse(lse)
+        if out is None:
+            out = tuple(torch.empty(s, dtype=self.dtype, device=self.device)
+                        for s in (self.q_shape, self.kv_shape, self.kv_shape))
+        else:
+            for t, kv, name in zip(out, (False, True, True), ("dq", "dk", "dv")):
+                self._view(t, kv, name)
+        dq, dk, dv = out
+        keep, views = _views(q, k, v, o, d_o, dq, dk, dv)
+        masks = self._masks(kv_len, key_mask)
+        ws, keep_ws = self._workspace(workspace, self.backward_ws)
+        with torch.cuda.device(self.device):
+            _check(load().bsa_cross_attention_backward(
+                self._h, *views[:3], *masks, views[3], lse.data_ptr(), *views[4:], *ws,
+                None if dev_status is None else dev_status.data_ptr(), _stream(self.device)))
+        return dq, dk, dv
+
+    def check_status(self):
+        """Synchronise the current stream and raise if a kernel recorded an error."""
+        with torch.cuda.device(self.device):
+            _check(load().bsa_cross_check_status(self._h, _stream(self.device)))
 
 
 def aggregation_scores(plans, x):

@@ -1,0 +1,55 @@
+// cross.cuh — argument block and launchers of the cross attention kernels
+// (internal; the public interface is include/bsa.h).
+#pragma once
+#include "common.cuh"
+#include "views.cuh"
+
+namespace bsa {
+
+// One cross attention.  Rows are the (head, token) pairs of Q that share one
+// head of K and V: row r of K/V head hk is head hk * group + r / n_q, token
+// r % n_q.  Per-row buffers are indexed by (b * heads + head) * n_q + token,
+// which for one (b, hk) is a contiguous range in the order of r.
+struct CrossArgs {
+  View q, k, v, o, d_o, dq, dk, dv;
+  const int32_t* kv_len;     // [B] or null
+  const uint8_t* key_mask;   // [B, n_kv] or null
+  float* lse;                // [B, heads, n_q] (forward: out or null)
+  float* delta;              // [B, heads, n_q] row sums of d_o * o (backward)
+  // Key-split partials of the forward: split s of a row holds the unnormalised
+  // output, its maximum in log2 units and its sum.
+  float* part_o;             // [splits, rows, D]
+  float2* part_ml;           // [splits, rows]
+  // Row-split partials of dK and dV: [splits, 2, B, heads_kv, n_kv, D].
+  float* part_kv;
+  int B, n_q, n_kv, heads, heads_kv, group;
+  int splits;                // of the kernel at hand
+  int split_len;             // key tiles (forward) or row tiles (dK, dV) per split
+  float scale, scale_log2;   // softmax scale, and times log2(e)
+  int32_t* status;
+};
+
+__host__ __device__ __forceinline__ long long cross_rows(const CrossArgs& a) {
+  return (long long)a.B * a.heads * a.n_q;
+}
+
+// Keys of batch element b that can be attended: kv_len[b], clamped to [0, n_kv]
+// (and recorded, status BSA_ERR_BAD_INDEX, where that changes it).
+__device__ __forceinline__ int cross_keys(const CrossArgs& a, int b) {
+  if (a.kv_len == nullptr) return a.n_kv;
+  const int n = __ldg(a.kv_len + b), c = min(max(n, 0), a.n_kv);
+  if (c != n) atomicCAS(a.status, 0, (int)BSA_ERR_BAD_INDEX);
+  return c;
+}
+
+// cross_simt.cu (fp32)
+constexpr int kCrossSimtTile = 64;   // rows and keys of a tile
+cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+cudaError_t launch_cross_simt_dq(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+cudaError_t launch_cross_simt_dkv(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+// cross_aux.cu
+cudaError_t launch_cross_merge(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+cudaError_t launch_cross_delta(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+cudaError_t launch_cross_reduce_kv(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+
+}  // namespace bsa

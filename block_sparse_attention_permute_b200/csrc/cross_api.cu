@@ -1,0 +1,221 @@
+// cross_api.cu — the C ABI of cross attention (bsa_cross_*): argument checks,
+// the split of each launch, workspace carving and launches.
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "bsa.h"
+#include "cross.cuh"
+
+struct bsa_cross_s {
+  int B, n_q, n_kv, heads, heads_kv, D;
+  bsa_dtype dtype;
+  int device;
+  float scale, scale_log2;
+  int32_t* d_status;
+  int fwd_splits, fwd_len;   // key splits of the forward, key tiles in each
+  int dkv_splits, dkv_len;   // row splits of dK and dV, row tiles in each
+};
+
+namespace {
+
+bsa_status fail(bsa_status s, const char* msg) { return bsa_internal_fail(s, msg); }
+bsa_status cuda_fail(cudaError_t e) { return fail(BSA_ERR_CUDA, cudaGetErrorString(e)); }
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Splits `units` of work of each of `ctas` CTAs over several CTAs when that
+// shortens the call: `slots` CTAs run at a time, and a CTA costs its units and
+// about `extra` units to start, write its partial and have it merged.  Returns
+// the units per split.
+int split_units(long long ctas, long long units, int slots, double extra) {
+  long long best = units;
+  double cost = (double)((ctas + slots - 1) / slots) * (units + (units > 1 ? 0.5 * extra : 0.0));
+  for (int s = 2; s <= 128 && s <= units; ++s) {
+    const long long len = (units + s - 1) / s, n = (units + len - 1) / len;
+    const double c = (double)((ctas * n + slots - 1) / slots) * (len + extra);
+    if (c < cost) cost = c, best = len;
+  }
+  return (int)best;
+}
+
+size_t rows_of(const bsa_cross_s* p) { return (size_t)p->B * p->heads * p->n_q; }
+
+size_t forward_bytes(const bsa_cross_s* p) {
+  if (p->fwd_splits == 1) return 0;
+  return round256((size_t)p->fwd_splits * rows_of(p) * p->D * sizeof(float)) +
+         round256((size_t)p->fwd_splits * rows_of(p) * sizeof(float2));
+}
+
+size_t backward_bytes(const bsa_cross_s* p) {
+  size_t n = round256(rows_of(p) * sizeof(float));
+  if (p->dkv_splits > 1)
+    n += round256((size_t)p->dkv_splits * 2 * p->B * p->heads_kv * p->n_kv * p->D * sizeof(float));
+  return n;
+}
+
+bsa_status check_cross(const bsa_cross_s* p) {
+  if (p == nullptr) return fail(BSA_ERR_INVALID_ARG, "cross is NULL");
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev != p->device) return fail(BSA_ERR_INVALID_ARG, "cross was created on another device than the current one");
+  return BSA_OK;
+}
+
+bsa_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return BSA_OK;
+  if (ws == nullptr || have < need) return fail(BSA_ERR_WORKSPACE, "workspace is missing or smaller than bsa_cross_workspace_size says");
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(BSA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  return BSA_OK;
+}
+
+// The views and scalars that both directions take.
+bsa_status fill(const bsa_cross_s* p, const bsa_view_t* q, const bsa_view_t* k, const bsa_view_t* v,
+                const bsa_view_t* o, bool o_written, const int32_t* kv_len, const uint8_t* key_mask,
+                int32_t* dev_status, bsa::CrossArgs* a) {
+  std::memset(a, 0, sizeof(*a));
+  const int esz = p->dtype == BSA_BF16 ? 2 : 4;
+  bsa_status s;
+  if ((s = bsa::check_view(q, "q", p->B, p->n_q, p->heads, p->D, esz, false, &a->q)) != BSA_OK) return s;
+  if ((s = bsa::check_view(k, "k", p->B, p->n_kv, p->heads_kv, p->D, esz, false, &a->k)) != BSA_OK) return s;
+  if ((s = bsa::check_view(v, "v", p->B, p->n_kv, p->heads_kv, p->D, esz, false, &a->v)) != BSA_OK) return s;
+  if ((s = bsa::check_view(o, "o", p->B, p->n_q, p->heads, p->D, esz, o_written, &a->o)) != BSA_OK) return s;
+  if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return fail(BSA_ERR_INVALID_ARG, "kv_len must be 4-byte aligned");
+  a->kv_len = kv_len;
+  a->key_mask = key_mask;
+  a->B = p->B; a->n_q = p->n_q; a->n_kv = p->n_kv; a->heads = p->heads; a->heads_kv = p->heads_kv;
+  a->group = p->heads / p->heads_kv;
+  a->scale = p->scale;
+  a->scale_log2 = p->scale_log2;
+  a->status = dev_status ? dev_status : p->d_status;
+  return BSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int heads, int heads_kv, int head_dim,
+                            bsa_dtype dtype, double scale) {
+  if (out == nullptr) return fail(BSA_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (batch < 1 || n_q < 1 || n_kv < 1) return fail(BSA_ERR_INVALID_ARG, "batch, n_q and n_kv must be >= 1");
+  if (heads < 1 || heads > BSA_MAX_HEADS || heads_kv < 1 || heads % heads_kv)
+    return fail(BSA_ERR_INVALID_ARG, "heads must be in [1, 256] and a multiple of heads_kv >= 1");
+  if (head_dim != 64 && head_dim != 128) return fail(BSA_ERR_INVALID_ARG, "head_dim must be 64 or 128");
+  if (dtype != BSA_F32 && dtype != BSA_BF16) return fail(BSA_ERR_INVALID_ARG, "bad dtype");
+  if (!(scale >= 0.0) || !std::isfinite(scale)) return fail(BSA_ERR_INVALID_ARG, "scale must be >= 0");
+  if ((long long)batch * heads * (n_q > n_kv ? n_q : n_kv) >= (1ll << 31))
+    return fail(BSA_ERR_UNSUPPORTED, "problem exceeds 2^31 rows");
+  bsa_cross_s c;
+  std::memset(&c, 0, sizeof(c));
+  c.B = batch; c.n_q = n_q; c.n_kv = n_kv; c.heads = heads; c.heads_kv = heads_kv; c.D = head_dim;
+  c.dtype = dtype;
+  const double sc = scale > 0.0 ? scale : 1.0 / std::sqrt((double)head_dim);
+  c.scale = (float)sc;
+  c.scale_log2 = (float)(sc * 1.4426950408889634);
+  const long long kT = bsa::kCrossSimtTile, bh = (long long)batch * heads_kv;
+  const long long row_tiles = ((long long)(heads / heads_kv) * n_q + kT - 1) / kT, key_tiles = (n_kv + kT - 1) / kT;
+  c.fwd_len = split_units(row_tiles * bh, key_tiles, 2 * 148, 1.0);
+  c.fwd_splits = (int)((key_tiles + c.fwd_len - 1) / c.fwd_len);
+  c.dkv_len = split_units(key_tiles * bh, row_tiles, 148, 1.0);
+  c.dkv_splits = (int)((row_tiles + c.dkv_len - 1) / c.dkv_len);
+  cudaError_t e = cudaGetDevice(&c.device);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if ((e = cudaMalloc(&c.d_status, sizeof(int32_t))) != cudaSuccess) return cuda_fail(e);
+  if ((e = cudaMemset(c.d_status, 0, sizeof(int32_t))) != cudaSuccess ||
+      (e = cudaStreamSynchronize(nullptr)) != cudaSuccess) {
+    cudaFree(c.d_status);
+    return cuda_fail(e);
+  }
+  *out = new (std::nothrow) bsa_cross_s(c);
+  if (*out == nullptr) {
+    cudaFree(c.d_status);
+    return fail(BSA_ERR_CUDA, "out of host memory");
+  }
+  return BSA_OK;
+}
+
+bsa_status bsa_cross_destroy(bsa_cross_t p) {
+  if (p == nullptr) return BSA_OK;
+  cudaFree(p->d_status);
+  delete p;
+  return BSA_OK;
+}
+
+bsa_status bsa_cross_workspace_size(bsa_cross_t p, size_t* forward_ws, size_t* backward_ws) {
+  if (p == nullptr) return fail(BSA_ERR_INVALID_ARG, "cross is NULL");
+  if (forward_ws) *forward_ws = forward_bytes(p);
+  if (backward_ws) *backward_ws = backward_bytes(p);
+  return BSA_OK;
+}
+
+bsa_status bsa_cross_attention(bsa_cross_t p, const bsa_view_t* q, const bsa_view_t* k, const bsa_view_t* v,
+                               const int32_t* kv_len, const uint8_t* key_mask, const bsa_view_t* o, float* lse,
+                               void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  bsa_status s = check_cross(p);
+  if (s != BSA_OK) return s;
+  bsa::CrossArgs a;
+  if ((s = fill(p, q, k, v, o, true, kv_len, key_mask, dev_status, &a)) != BSA_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, forward_bytes(p))) != BSA_OK) return s;
+  a.lse = lse;
+  a.splits = p->fwd_splits;
+  a.split_len = p->fwd_len;
+  if (a.splits > 1) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) +
+                                          round256((size_t)a.splits * rows_of(p) * p->D * sizeof(float)));
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool is_bf16 = p->dtype == BSA_BF16;
+  cudaError_t e = bsa::launch_cross_simt_forward(a, p->D, is_bf16, st);
+  if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_merge(a, p->D, is_bf16, st);
+  return e == cudaSuccess ? BSA_OK : cuda_fail(e);
+}
+
+bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, const bsa_view_t* k, const bsa_view_t* v,
+                                        const int32_t* kv_len, const uint8_t* key_mask, const bsa_view_t* o,
+                                        const float* lse, const bsa_view_t* d_o, const bsa_view_t* dq,
+                                        const bsa_view_t* dk, const bsa_view_t* dv, void* ws, size_t ws_bytes,
+                                        int32_t* dev_status, void* stream) {
+  bsa_status s = check_cross(p);
+  if (s != BSA_OK) return s;
+  bsa::CrossArgs a;
+  if ((s = fill(p, q, k, v, o, false, kv_len, key_mask, dev_status, &a)) != BSA_OK) return s;
+  const int esz = p->dtype == BSA_BF16 ? 2 : 4;
+  if ((s = bsa::check_view(d_o, "d_o", p->B, p->n_q, p->heads, p->D, esz, false, &a.d_o)) != BSA_OK) return s;
+  if ((s = bsa::check_view(dq, "dq", p->B, p->n_q, p->heads, p->D, esz, true, &a.dq)) != BSA_OK) return s;
+  if ((s = bsa::check_view(dk, "dk", p->B, p->n_kv, p->heads_kv, p->D, esz, true, &a.dk)) != BSA_OK) return s;
+  if ((s = bsa::check_view(dv, "dv", p->B, p->n_kv, p->heads_kv, p->D, esz, true, &a.dv)) != BSA_OK) return s;
+  if (lse == nullptr) return fail(BSA_ERR_INVALID_ARG, "lse is NULL");
+  if (a.dq.p == a.dk.p || a.dq.p == a.dv.p || a.dk.p == a.dv.p)
+    return fail(BSA_ERR_INVALID_ARG, "dq, dk and dv are the same memory");
+  if ((s = check_ws(ws, ws_bytes, backward_bytes(p))) != BSA_OK) return s;
+  a.lse = const_cast<float*>(lse);
+  a.delta = static_cast<float*>(ws);
+  a.part_kv = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(rows_of(p) * sizeof(float)));
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool is_bf16 = p->dtype == BSA_BF16;
+  cudaError_t e = bsa::launch_cross_delta(a, p->D, is_bf16, st);
+  if (e == cudaSuccess) e = bsa::launch_cross_simt_dq(a, p->D, is_bf16, st);
+  a.splits = p->dkv_splits;
+  a.split_len = p->dkv_len;
+  if (e == cudaSuccess) e = bsa::launch_cross_simt_dkv(a, p->D, is_bf16, st);
+  if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_reduce_kv(a, p->D, is_bf16, st);
+  return e == cudaSuccess ? BSA_OK : cuda_fail(e);
+}
+
+bsa_status bsa_cross_check_status(bsa_cross_t p, void* stream) {
+  bsa_status s = check_cross(p);
+  if (s != BSA_OK) return s;
+  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+  int32_t v = 0;
+  if (e == cudaSuccess) e = cudaMemcpy(&v, p->d_status, sizeof(v), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemset(p->d_status, 0, sizeof(v));
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (v == 0) return BSA_OK;
+  return fail((bsa_status)v, v == BSA_ERR_TIMEOUT ? "kernel reported that a bounded wait ran out"
+                                                   : "kernel reported a kv_len outside [0, n_kv]");
+}
+
+}  // extern "C"

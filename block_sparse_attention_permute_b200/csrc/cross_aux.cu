@@ -1,0 +1,127 @@
+// cross_aux.cu — the memory-bound passes around the cross attention kernels:
+// the merge of key splits, the row sums of d_o * o, the sum of row splits.
+#include "cross.cuh"
+
+namespace bsa {
+namespace {
+
+template <typename T> __device__ __forceinline__ float4 in4(const T* p);
+template <> __device__ __forceinline__ float4 in4<float>(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <> __device__ __forceinline__ float4 in4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void out4(float* d, float4 x) { *reinterpret_cast<float4*>(d) = x; }
+__device__ __forceinline__ void out4(__nv_bfloat16* d, float4 x) {
+  *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+
+// (b, head, token) of row `at` of a per-row buffer.
+__device__ __forceinline__ void row_of(const CrossArgs& a, long long at, int& b, int& h, int& n) {
+  const long long bh = at / a.n_q;
+  n = (int)(at - bh * a.n_q);
+  b = (int)(bh / a.heads);
+  h = (int)(bh - (long long)b * a.heads);
+}
+
+// A group of D / 4 threads per row.  With partials (O_s, m_s, l_s) of the key
+// splits: M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s, and
+// lse = ln 2 (M + log2 sum w_s l_s).  Splits are taken in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_merge(CrossArgs a) {
+  constexpr int G = D / 4;
+  const long long rows = cross_rows(a), at = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
+  if (at >= rows) return;
+  const int c = (threadIdx.x % G) * 4;
+  float M = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[s * rows + at].x);
+  const float base = M == -INFINITY ? 0.f : M;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 ml = a.part_ml[s * rows + at];
+    const float w = exp2f(ml.x - base);
+    const float4 x = in4(a.part_o + (s * rows + at) * D + c);
+    l = fmaf(w, ml.y, l);
+    acc = make_float4(fmaf(w, x.x, acc.x), fmaf(w, x.y, acc.y), fmaf(w, x.z, acc.z), fmaf(w, x.w, acc.w));
+  }
+  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+  int b, h, n;
+  row_of(a, at, b, h, n);
+  out4(reinterpret_cast<T*>(a.o.p) + b * a.o.b + n * a.o.n + h * a.o.h + c,
+       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (c == 0 && a.lse) a.lse[at] = (M + log2f(l)) * 0.69314718055994531f;
+}
+
+// A group of D / 4 threads per (token, head) row; neighbouring groups take
+// neighbouring heads of a token.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_delta(CrossArgs a) {
+  constexpr int G = D / 4;
+  const long long rows = cross_rows(a), id = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
+  float sum = 0.f;
+  int b = 0, h = 0, n = 0;
+  if (id < rows) {
+    const long long bn = id / a.heads;
+    h = (int)(id - bn * a.heads);
+    b = (int)(bn / a.n_q);
+    n = (int)(bn - (long long)b * a.n_q);
+    const int c = (threadIdx.x % G) * 4;
+    const float4 x = in4(reinterpret_cast<const T*>(a.o.p) + b * a.o.b + n * a.o.n + h * a.o.h + c);
+    const float4 y = in4(reinterpret_cast<const T*>(a.d_o.p) + b * a.d_o.b + n * a.d_o.n + h * a.d_o.h + c);
+    sum = x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+  }
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (id < rows && threadIdx.x % G == 0) a.delta[((long long)b * a.heads + h) * a.n_q + n] = sum;
+}
+
+// dK and dV from the partials of the row splits, added in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_reduce_kv(CrossArgs a) {
+  const long long all = (long long)a.B * a.heads_kv * a.n_kv;
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x, at = id / (D / 4);
+  if (at >= all) return;
+  const int c = (int)(id % (D / 4)) * 4, which = blockIdx.y;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.splits; ++s) {
+    const float4 x = in4(a.part_kv + ((2ll * s + which) * all + at) * D + c);
+    acc = make_float4(acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w);
+  }
+  const long long bh = at / a.n_kv;
+  const int j = (int)(at - bh * a.n_kv), b = (int)(bh / a.heads_kv), hk = (int)(bh % a.heads_kv);
+  const View& v = which ? a.dv : a.dk;
+  out4(reinterpret_cast<T*>(v.p) + b * v.b + j * v.n + hk * v.h + c, acc);
+}
+
+template <typename T, int D>
+cudaError_t run_aux(int which, const CrossArgs& a, cudaStream_t st) {
+  const long long rows = cross_rows(a), keys = (long long)a.B * a.heads_kv * a.n_kv;
+  const unsigned row_ctas = (unsigned)((rows + 1024 / D - 1) / (1024 / D));
+  if (which == 0) cross_merge<T, D><<<row_ctas, 256, 0, st>>>(a);
+  else if (which == 1) cross_delta<T, D><<<row_ctas, 256, 0, st>>>(a);
+  else cross_reduce_kv<T, D><<<dim3((unsigned)((keys * (D / 4) + 255) / 256), 2), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t run_aux(int which, const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
+  if (is_bf16) return D == 128 ? run_aux<__nv_bfloat16, 128>(which, a, st) : run_aux<__nv_bfloat16, 64>(which, a, st);
+  return D == 128 ? run_aux<float, 128>(which, a, st) : run_aux<float, 64>(which, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_cross_merge(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
+  return run_aux(0, a, D, is_bf16, st);
+}
+cudaError_t launch_cross_delta(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
+  return run_aux(1, a, D, is_bf16, st);
+}
+cudaError_t launch_cross_reduce_kv(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
+  return run_aux(2, a, D, is_bf16, st);
+}
+
+}  // namespace bsa

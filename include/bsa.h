@@ -573,6 +573,68 @@ bsa_status bsa_rotary(bsa_rope_t rope, const bsa_view_t* q, const bsa_view_t* k,
                       const bsa_view_t* q_out, const bsa_view_t* k_out,
                       const int64_t* t_origin, int backward, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Cross attention: O = softmax(scale Q K^T) V over the keys of each batch
+ * element, from n_q query tokens to n_kv encoder states; head h of Q reads
+ * head h / (heads / heads_kv) of K and V.  A key is attended if it is below
+ * kv_len[b] and its key_mask byte is not 0; what K and V hold at the other
+ * keys (also infinities and NaN) does not enter.  A batch element without
+ * attended keys gives O = 0, lse = -inf and zero gradients. */
+typedef struct bsa_cross_s* bsa_cross_t;
+
+/* bsa_cross_create — sizes of one cross attention.
+ *   batch, n_q, n_kv >= 1; heads in [1, 256], a multiple of heads_kv >= 1;
+ *   head_dim in {64, 128}; dtype; scale > 0, or 0 for 1 / sqrt(head_dim);
+ *   batch * heads * max(n_q, n_kv) below 2^31.
+ * BSA_BF16 runs on the tensor cores (probabilities and their gradients are
+ * rounded to bf16 as operands, every sum is fp32), BSA_F32 in fp32 throughout.
+ * The object holds a status word on the current device. */
+bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv,
+                            int heads, int heads_kv, int head_dim,
+                            bsa_dtype dtype, double scale);
+bsa_status bsa_cross_destroy(bsa_cross_t cross);
+
+/* bsa_cross_workspace_size — bytes of device workspace of the two calls below
+ * (either may come out as 0).  A call overwrites its workspace; calls that may
+ * overlap on the GPU need one each. */
+bsa_status bsa_cross_workspace_size(bsa_cross_t cross, size_t* forward_ws,
+                                    size_t* backward_ws);
+
+/* bsa_cross_attention — forward.
+ *   q, o      [B, n_q, heads, D] views;  k, v  [B, n_kv, heads_kv, D] views
+ *   kv_len    device int32 [B] or NULL (n_kv); a value outside [0, n_kv] is
+ *             clamped and recorded as BSA_ERR_BAD_INDEX
+ *   key_mask  device uint8 [B, n_kv] or NULL (all attended)
+ *   lse       device float [B, heads, n_q] out, or NULL: log of the sum of the
+ *             exponentials (natural log), as the backward needs it
+ *   ws        256-byte aligned, >= forward_ws (may be NULL if that is 0)
+ *   dev_status  as for bsa_attention (NULL = the object's own word)
+ * Captures into a CUDA graph. */
+bsa_status bsa_cross_attention(bsa_cross_t cross, const bsa_view_t* q,
+                               const bsa_view_t* k, const bsa_view_t* v,
+                               const int32_t* kv_len, const uint8_t* key_mask,
+                               const bsa_view_t* o, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status,
+                               void* stream);
+
+/* bsa_cross_attention_backward — gradients from d_o [B, n_q, heads, D].
+ *   q, k, v, kv_len, key_mask  as in the forward;  o, lse  its outputs
+ *   dq [B, n_q, heads, D], dk, dv [B, n_kv, heads_kv, D]  view outputs, every
+ *   element written (dk and dv summed over the heads that share them; zero at
+ *   keys that are not attended)
+ *   ws  >= backward_ws
+ * Every sum has a fixed order: two calls on the same inputs agree bit for
+ * bit. */
+bsa_status bsa_cross_attention_backward(
+    bsa_cross_t cross, const bsa_view_t* q, const bsa_view_t* k,
+    const bsa_view_t* v, const int32_t* kv_len, const uint8_t* key_mask,
+    const bsa_view_t* o, const float* lse, const bsa_view_t* d_o,
+    const bsa_view_t* dq, const bsa_view_t* dk, const bsa_view_t* dv, void* ws,
+    size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* bsa_cross_check_status — bsa_check_status for the object's status word. */
+bsa_status bsa_cross_check_status(bsa_cross_t cross, void* stream);
+
 /* bsa_check_status — synchronise `stream`, read and clear the plan-owned
  * status word; returns BSA_OK or the recorded error. */
 bsa_status bsa_check_status(bsa_plan_t plan, void* stream);

@@ -123,3 +123,31 @@ def test_binding_fails_loudly_without_library(monkeypatch):
 def test_binding_rejects_cpu_device():
     with pytest.raises(bsa.BsaError):
         bsa.Plan(1, 4, 8, 8, 2, 4, 4, 2, 64, device="cpu")
+
+
+def test_rope_and_cross_reject_bad_arguments(lib):
+    h = ctypes.c_void_p()
+    assert lib.bsa_rope_create(None, None, None) == 1
+    cfg = bsa.RopeConfig()
+    assert lib.bsa_rope_create(ctypes.byref(h), None, None) == 1
+    cfg.dim[:] = (3, 0, 0)
+    assert lib.bsa_rope_create(ctypes.byref(h), None, ctypes.byref(cfg)) == 1
+    assert "even" in lib.bsa_last_error_string().decode()
+    cfg.dim[:] = (4, 0, 0)
+    cfg.theta = 1.0
+    assert lib.bsa_rope_create(ctypes.byref(h), None, ctypes.byref(cfg)) == 1
+    assert "theta" in lib.bsa_last_error_string().decode()
+    assert lib.bsa_rotary(None, None, None, None, None, None, 0, None) == 1
+    assert lib.bsa_rope_destroy(None) == 0
+    for args, needle in (((1, 0, 4, 2, 2, 64, 1, 0.0), "n_q"), ((1, 4, 0, 2, 2, 64, 1, 0.0), "n_kv"),
+                         ((1, 4, 4, 3, 2, 64, 1, 0.0), "multiple"), ((1, 4, 4, 257, 1, 64, 1, 0.0), "heads"),
+                         ((1, 4, 4, 2, 2, 96, 1, 0.0), "head_dim"), ((1, 4, 4, 2, 2, 64, 5, 0.0), "dtype"),
+                         ((1, 4, 4, 2, 2, 64, 1, -1.0), "scale"), ((1, 4, 4, 2, 2, 64, 1, float("nan")), "scale")):
+        assert lib.bsa_cross_create(ctypes.byref(h), *args) == 1
+        assert needle in lib.bsa_last_error_string().decode()
+    assert lib.bsa_cross_create(ctypes.byref(h), 1 << 15, 1 << 10, 4, 64, 64, 64, 1, 0.0) == 2
+    assert lib.bsa_cross_destroy(None) == 0
+    assert lib.bsa_cross_workspace_size(None, None, None) == 1
+    assert lib.bsa_cross_attention(*[None] * 9, 0, None, None) == 1
+    assert lib.bsa_cross_attention_backward(*[None] * 13, 0, None, None) == 1
+    assert lib.bsa_cross_check_status(None, None) == 1
