@@ -102,6 +102,7 @@ def load():
         "bsa_cross_attention": [P] * 9 + [Z, P, P],
         "bsa_cross_attention_backward": [P] * 13 + [Z, P, P],
         "bsa_cross_check_status": [P, P],
+        "bsa_cross_set_watchdog": [P, ctypes.c_longlong, I],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -715,6 +716,11 @@ class CrossAttention:
         """Synchronise the current stream and raise if a kernel recorded an error."""
         with torch.cuda.device(self.device):
             _check(load().bsa_cross_check_status(self._h, _stream(self.device)))
+
+    def set_watchdog(self, wait_limit_cycles=0, withhold_copy=0):
+        """Bound of the tensor-core kernels' waits (0 = default, about a second) and the timeout
+        path's test hook (bsa_cross_set_watchdog)."""
+        _check(load().bsa_cross_set_watchdog(self._h, int(wait_limit_cycles), int(withhold_copy)))
 
 
 def aggregation_scores(plans, x):

@@ -1244,3 +1244,11 @@ bsa_status bsa_internal_plan_sizes(bsa_plan_t p, const Geo** g, int* is_bf16, in
   *device = p->device;
   return BSA_OK;
 }
+
+// A tiled bf16 tensor map with the 128-byte swizzle (for cross_api.cu).
+bsa_status bsa_internal_tile_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                                 const cuuint64_t* strides, const cuuint32_t* box) {
+  if (encode_fn() == nullptr) return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const CUresult r = encode(m, base, rank, dims, strides, box);
+  return r == CUDA_SUCCESS ? BSA_OK : fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}

@@ -42,6 +42,28 @@ __device__ __forceinline__ int cross_keys(const CrossArgs& a, int b) {
   return c;
 }
 
+// Schedule of the tensor-core kernels.  A query tile is 128 rows: `tokens`
+// tokens of `pack` heads that share a K/V head (few tokens: more heads, so that
+// fewer rows are empty), heads fastest.
+struct CrossTiles {
+  int tiles;        // query tiles of one (batch element, K/V head)
+  int tokens, pack; // tokens * pack <= 128
+  int shared;       // streams take two query tiles over the same keys (else one over two key runs)
+  int items;        // (batch element, K/V head, split, item of it), the last fastest
+  int ctas;         // CTAs at a time (one per SM)
+  FastDiv div_items, div_splits, div_hkv, div_tok, div_pack;
+  int step_qb, step_qh, step_kb, step_kh, step_vb, step_vh;   // 0 along an axis the view repeats, else 1
+  long long wait_limit;   // bound of every in-kernel wait, SM cycles (0 = default)
+  int hold_load;          // test hook: n > 0 = CTA 0 never issues its n-th K/V copy
+};
+// Tensor maps (d, head, token, batch) of the views.
+struct CrossMaps {
+  CUtensorMap q, k, v, d_o;
+};
+
+// cross_tc.cu (bf16)
+cudaError_t launch_cross_tc_forward(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D,
+                                    cudaStream_t st);
 // cross_simt.cu (fp32)
 constexpr int kCrossSimtTile = 64;   // rows and keys of a tile
 cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);

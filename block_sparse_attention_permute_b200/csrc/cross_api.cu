@@ -7,13 +7,19 @@
 #include "bsa.h"
 #include "cross.cuh"
 
+bsa_status bsa_internal_tile_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                                 const cuuint64_t* strides, const cuuint32_t* box);
+
 struct bsa_cross_s {
   int B, n_q, n_kv, heads, heads_kv, D;
   bsa_dtype dtype;
   int device;
   float scale, scale_log2;
   int32_t* d_status;
-  int fwd_splits, fwd_len;   // key splits of the forward, key tiles in each
+  long long wait_limit;      // bound of the tensor-core kernels' waits, SM cycles (0 = default)
+  int hold_load;             // test hook of the timeout path (0 = off)
+  bsa::CrossTiles fwd;       // schedule of the forward (bf16)
+  int fwd_splits, fwd_len;   // partials of a row in the forward, key tiles per split
   int dkv_splits, dkv_len;   // row splits of dK and dV, row tiles in each
 };
 
@@ -24,18 +30,71 @@ bsa_status cuda_fail(cudaError_t e) { return fail(BSA_ERR_CUDA, cudaGetErrorStri
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Splits `units` of work of each of `ctas` CTAs over several CTAs when that
-// shortens the call: `slots` CTAs run at a time, and a CTA costs its units and
-// about `extra` units to start, write its partial and have it merged.  Returns
-// the units per split.
-int split_units(long long ctas, long long units, int slots, double extra) {
-  long long best = units;
-  double cost = (double)((ctas + slots - 1) / slots) * (units + (units > 1 ? 0.5 * extra : 0.0));
+// shortens the call: `slots` CTAs run at a time, and a split call costs its CTAs
+// about `extra` units more, to write the partials and to merge them.  Returns
+// the units per split, *cost its estimate.
+int split_units(long long ctas, long long units, int slots, double extra, double* cost = nullptr) {
+  long long len = units;
+  double best = (double)((ctas + slots - 1) / slots) * units;
   for (int s = 2; s <= 128 && s <= units; ++s) {
-    const long long len = (units + s - 1) / s, n = (units + len - 1) / len;
-    const double c = (double)((ctas * n + slots - 1) / slots) * (len + extra);
-    if (c < cost) cost = c, best = len;
+    const long long l = (units + s - 1) / s, n = (units + l - 1) / l;
+    const double c = (double)((ctas * n + slots - 1) / slots) * l + extra;
+    if (c < best) best = c, len = l;
   }
-  return (int)best;
+  if (cost) *cost = best;
+  return (int)len;
+}
+
+constexpr int kSms = 148;
+
+// The forward's schedule on the tensor cores.
+void plan_forward(bsa_cross_s* c) {
+  bsa::CrossTiles& t = c->fwd;
+  const int group = c->heads / c->heads_kv;
+  const long long bh = (long long)c->B * c->heads_kv;
+  // heads packed into a tile: the divisor of the group that leaves the fewest tiles
+  long long tiles = 0;
+  for (int p = 1; p <= group && p <= 128; ++p) {
+    if (group % p) continue;
+    const int tokens = 128 / p;
+    const long long n = (long long)(group / p) * ((c->n_q + tokens - 1) / tokens);
+    if (tiles == 0 || n < tiles) tiles = n, t.pack = p, t.tokens = tokens;
+  }
+  t.tiles = (int)tiles;
+  const int key_tiles = (c->n_kv + 127) / 128;
+  // Two tiles per item over the same keys, or one tile over two runs of keys
+  // (always merged): whichever the estimate says ends first, a round of both
+  // streams being the unit and partials and merge costing about three rounds.
+  double pair, dual;
+  const int len = split_units(bh * ((tiles + 1) / 2), key_tiles, kSms, 3.0, &pair);
+  const int half = split_units(bh * tiles, (key_tiles + 1) / 2, kSms, 0.0, &dual);
+  t.shared = key_tiles == 1 || pair <= dual + 3.0;
+  c->fwd_len = t.shared ? len : 2 * half;
+  const int splits = (key_tiles + c->fwd_len - 1) / c->fwd_len;
+  c->fwd_splits = t.shared ? splits : 2 * splits;
+  const int per = (int)(t.shared ? (tiles + 1) / 2 : tiles);
+  t.items = (int)(bh * per * splits);
+  t.ctas = kSms;
+  t.div_items = make_fastdiv((uint32_t)per);
+  t.div_splits = make_fastdiv((uint32_t)splits);
+  t.div_hkv = make_fastdiv((uint32_t)c->heads_kv);
+  t.div_tok = make_fastdiv((uint32_t)((c->n_q + t.tokens - 1) / t.tokens));
+  t.div_pack = make_fastdiv((uint32_t)t.pack);
+}
+
+// Map (d, head, token, batch) of a [B, n, heads, D] bf16 view with a box of 64
+// elements x `pack` heads x `tokens` tokens.  An axis that the view repeats
+// (stride 0) becomes one of length 1, its coordinate then stays 0.
+bsa_status make_map(CUtensorMap* m, const bsa::View& v, int B, int n, int heads, int D, int pack, int tokens,
+                    int* step_b, int* step_h) {
+  *step_b = v.b ? 1 : 0;
+  *step_h = v.h ? 1 : 0;
+  const cuuint64_t any = (cuuint64_t)D * 2;    // stride of an axis of length 1
+  const cuuint64_t dims[4] = {(cuuint64_t)D, v.h ? (cuuint64_t)heads : 1, (cuuint64_t)n, v.b ? (cuuint64_t)B : 1};
+  const cuuint64_t strides[3] = {v.h ? (cuuint64_t)v.h * 2 : any, v.n ? (cuuint64_t)v.n * 2 : any,
+                                 v.b ? (cuuint64_t)v.b * 2 : any};
+  const cuuint32_t box[4] = {64, (cuuint32_t)pack, (cuuint32_t)tokens, 1};
+  return bsa_internal_tile_map(m, v.p, 4, dims, strides, box);
 }
 
 size_t rows_of(const bsa_cross_s* p) { return (size_t)p->B * p->heads * p->n_q; }
@@ -80,6 +139,8 @@ bsa_status fill(const bsa_cross_s* p, const bsa_view_t* q, const bsa_view_t* k, 
   if ((s = bsa::check_view(k, "k", p->B, p->n_kv, p->heads_kv, p->D, esz, false, &a->k)) != BSA_OK) return s;
   if ((s = bsa::check_view(v, "v", p->B, p->n_kv, p->heads_kv, p->D, esz, false, &a->v)) != BSA_OK) return s;
   if ((s = bsa::check_view(o, "o", p->B, p->n_q, p->heads, p->D, esz, o_written, &a->o)) != BSA_OK) return s;
+  if ((p->n_q > 1 && a->q.n == 0) || (p->n_kv > 1 && (a->k.n == 0 || a->v.n == 0)))
+    return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no view that repeats its tokens (token stride 0)");
   if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return fail(BSA_ERR_INVALID_ARG, "kv_len must be 4-byte aligned");
   a->kv_len = kv_len;
   a->key_mask = key_mask;
@@ -94,6 +155,15 @@ bsa_status fill(const bsa_cross_s* p, const bsa_view_t* q, const bsa_view_t* k, 
 }  // namespace
 
 extern "C" {
+
+bsa_status bsa_cross_set_watchdog(bsa_cross_t p, long long wait_limit_cycles, int withhold_copy) {
+  if (p == nullptr) return fail(BSA_ERR_INVALID_ARG, "cross is NULL");
+  if (wait_limit_cycles < 0 || withhold_copy < 0)
+    return fail(BSA_ERR_INVALID_ARG, "wait limit and withheld copy must be >= 0");
+  p->wait_limit = wait_limit_cycles;
+  p->hold_load = withhold_copy;
+  return BSA_OK;
+}
 
 bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int heads, int heads_kv, int head_dim,
                             bsa_dtype dtype, double scale) {
@@ -116,9 +186,13 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   c.scale_log2 = (float)(sc * 1.4426950408889634);
   const long long kT = bsa::kCrossSimtTile, bh = (long long)batch * heads_kv;
   const long long row_tiles = ((long long)(heads / heads_kv) * n_q + kT - 1) / kT, key_tiles = (n_kv + kT - 1) / kT;
-  c.fwd_len = split_units(row_tiles * bh, key_tiles, 2 * 148, 1.0);
-  c.fwd_splits = (int)((key_tiles + c.fwd_len - 1) / c.fwd_len);
-  c.dkv_len = split_units(key_tiles * bh, row_tiles, 148, 1.0);
+  if (dtype == BSA_BF16) {
+    plan_forward(&c);
+  } else {
+    c.fwd_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 1.0);
+    c.fwd_splits = (int)((key_tiles + c.fwd_len - 1) / c.fwd_len);
+  }
+  c.dkv_len = split_units(key_tiles * bh, row_tiles, kSms, 1.0);
   c.dkv_splits = (int)((row_tiles + c.dkv_len - 1) / c.dkv_len);
   cudaError_t e = cudaGetDevice(&c.device);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -168,7 +242,21 @@ bsa_status bsa_cross_attention(bsa_cross_t p, const bsa_view_t* q, const bsa_vie
   }
   cudaStream_t st = (cudaStream_t)stream;
   const bool is_bf16 = p->dtype == BSA_BF16;
-  cudaError_t e = bsa::launch_cross_simt_forward(a, p->D, is_bf16, st);
+  cudaError_t e;
+  if (is_bf16) {
+    bsa::CrossMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    bsa::CrossTiles t = p->fwd;
+    if ((s = make_map(&maps.q, a.q, p->B, p->n_q, p->heads, p->D, t.pack, t.tokens, &t.step_qb, &t.step_qh)) != BSA_OK ||
+        (s = make_map(&maps.k, a.k, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t.step_kb, &t.step_kh)) != BSA_OK ||
+        (s = make_map(&maps.v, a.v, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t.step_vb, &t.step_vh)) != BSA_OK)
+      return s;
+    t.wait_limit = p->wait_limit;
+    t.hold_load = p->hold_load;
+    e = bsa::launch_cross_tc_forward(a, t, maps, p->D, st);
+  } else {
+    e = bsa::launch_cross_simt_forward(a, p->D, is_bf16, st);
+  }
   if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_merge(a, p->D, is_bf16, st);
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
 }

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(256) cross_merge(CrossArgs a) {
   float l = 0.f;
   for (int s = 0; s < a.splits; ++s) {
     const float2 ml = a.part_ml[s * rows + at];
+    if (ml.x == -INFINITY) continue;   // no key: its O is not written
     const float w = exp2f(ml.x - base);
     const float4 x = in4(a.part_o + (s * rows + at) * D + c);
     l = fmaf(w, ml.y, l);

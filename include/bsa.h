@@ -602,6 +602,7 @@ bsa_status bsa_cross_workspace_size(bsa_cross_t cross, size_t* forward_ws,
 
 /* bsa_cross_attention — forward.
  *   q, o      [B, n_q, heads, D] views;  k, v  [B, n_kv, heads_kv, D] views
+ *             (inputs may repeat along the batch or the heads, not the tokens)
  *   kv_len    device int32 [B] or NULL (n_kv); a value outside [0, n_kv] is
  *             clamped and recorded as BSA_ERR_BAD_INDEX
  *   key_mask  device uint8 [B, n_kv] or NULL (all attended)
@@ -631,6 +632,15 @@ bsa_status bsa_cross_attention_backward(
     const bsa_view_t* o, const float* lse, const bsa_view_t* d_o,
     const bsa_view_t* dq, const bsa_view_t* dk, const bsa_view_t* dv, void* ws,
     size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* bsa_cross_set_watchdog — bsa_plan_set_watchdog for the tensor-core kernels of
+ * the two calls: the bound of every in-kernel wait in SM cycles (0 = default,
+ * about a second) and the test hook (n > 0: the first CTA never issues its n-th
+ * K/V copy).  A wait that runs out ends the call with BSA_ERR_TIMEOUT in the
+ * status word; its outputs are then undefined. */
+bsa_status bsa_cross_set_watchdog(bsa_cross_t cross,
+                                  long long wait_limit_cycles,
+                                  int withhold_copy);
 
 /* bsa_cross_check_status — bsa_check_status for the object's status word. */
 bsa_status bsa_cross_check_status(bsa_cross_t cross, void* stream);
