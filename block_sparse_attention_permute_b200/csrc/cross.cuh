@@ -15,9 +15,10 @@ struct CrossArgs {
   const int32_t* kv_len;     // [B] or null
   const uint8_t* key_mask;   // [B, n_kv] or null
   float* lse;                // [B, heads, n_q] (forward: out or null)
-  float* delta;              // [B, heads, n_q] row sums of d_o * o (backward)
+  float* delta;              // [B, heads, n_q] row sums of d_o * o (fp32 backward)
+  float* stats;              // [query tiles][2][128]: -lse in log2 units (-inf: P = 0), -delta (bf16 backward)
   // Key-split partials of the forward: split s of a row holds the unnormalised
-  // output, its maximum in log2 units and its sum.
+  // output, its maximum in log2 units and its sum.  (Also the partials of dQ.)
   float* part_o;             // [splits, rows, D]
   float2* part_ml;           // [splits, rows]
   // Row-split partials of dK and dV: [splits, 2, B, heads_kv, n_kv, D].
@@ -52,7 +53,7 @@ struct CrossTiles {
   int items;        // (batch element, K/V head, split, item of it), the last fastest
   int ctas;         // CTAs at a time (one per SM)
   FastDiv div_items, div_splits, div_hkv, div_tok, div_pack;
-  int step_qb, step_qh, step_kb, step_kh, step_vb, step_vh;   // 0 along an axis the view repeats, else 1
+  int step_qb, step_qh, step_kb, step_kh, step_vb, step_vh, step_ob, step_oh;   // 0 along an axis the view repeats, else 1
   long long wait_limit;   // bound of every in-kernel wait, SM cycles (0 = default)
   int hold_load;          // test hook: n > 0 = CTA 0 never issues its n-th K/V copy
 };
@@ -64,14 +65,19 @@ struct CrossMaps {
 // cross_tc.cu (bf16)
 cudaError_t launch_cross_tc_forward(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D,
                                     cudaStream_t st);
+// cross_tc_bwd.cu (bf16; tiles with pack * tokens == 128)
+cudaError_t launch_cross_tc_dq(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st);
+cudaError_t launch_cross_tc_dkv(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st);
+cudaError_t launch_cross_stats(const CrossArgs& a, const CrossTiles& t, int D, cudaStream_t st);
 // cross_simt.cu (fp32)
 constexpr int kCrossSimtTile = 64;   // rows and keys of a tile
-cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
-cudaError_t launch_cross_simt_dq(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
-cudaError_t launch_cross_simt_dkv(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, cudaStream_t st);
+cudaError_t launch_cross_simt_dq(const CrossArgs& a, int D, cudaStream_t st);
+cudaError_t launch_cross_simt_dkv(const CrossArgs& a, int D, cudaStream_t st);
 // cross_aux.cu
 cudaError_t launch_cross_merge(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
-cudaError_t launch_cross_delta(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
+cudaError_t launch_cross_delta(const CrossArgs& a, int D, cudaStream_t st);   // fp32
+cudaError_t launch_cross_sum_q(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
 cudaError_t launch_cross_reduce_kv(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
 
 }  // namespace bsa

@@ -18,8 +18,9 @@ struct bsa_cross_s {
   int32_t* d_status;
   long long wait_limit;      // bound of the tensor-core kernels' waits, SM cycles (0 = default)
   int hold_load;             // test hook of the timeout path (0 = off)
-  bsa::CrossTiles fwd;       // schedule of the forward (bf16)
+  bsa::CrossTiles fwd, bwd;  // schedules of the forward, and of dQ (and the query tiles of dK, dV) (bf16)
   int fwd_splits, fwd_len;   // partials of a row in the forward, key tiles per split
+  int dq_splits, dq_len;     // key splits of dQ
   int dkv_splits, dkv_len;   // row splits of dK and dV, row tiles in each
 };
 
@@ -47,39 +48,57 @@ int split_units(long long ctas, long long units, int slots, double extra, double
 
 constexpr int kSms = 148;
 
-// The forward's schedule on the tensor cores.
-void plan_forward(bsa_cross_s* c) {
-  bsa::CrossTiles& t = c->fwd;
+// Query tiles of 128 rows: the divisor of the group that leaves the fewest
+// tiles is packed into one (`whole`: only divisors of 128, so that every row of
+// a tile is loaded).
+void plan_tiles(const bsa_cross_s* c, bool whole, bsa::CrossTiles* t) {
   const int group = c->heads / c->heads_kv;
-  const long long bh = (long long)c->B * c->heads_kv;
-  // heads packed into a tile: the divisor of the group that leaves the fewest tiles
   long long tiles = 0;
   for (int p = 1; p <= group && p <= 128; ++p) {
-    if (group % p) continue;
+    if (group % p || (whole && 128 % p)) continue;
     const int tokens = 128 / p;
     const long long n = (long long)(group / p) * ((c->n_q + tokens - 1) / tokens);
-    if (tiles == 0 || n < tiles) tiles = n, t.pack = p, t.tokens = tokens;
+    if (tiles == 0 || n < tiles) tiles = n, t->pack = p, t->tokens = tokens;
   }
-  t.tiles = (int)tiles;
+  t->tiles = (int)tiles;
+  t->ctas = kSms;
+  t->div_hkv = make_fastdiv((uint32_t)c->heads_kv);
+  t->div_tok = make_fastdiv((uint32_t)((c->n_q + t->tokens - 1) / t->tokens));
+  t->div_pack = make_fastdiv((uint32_t)t->pack);
+}
+
+// Items of a K/V head (`per` for each of `splits` key runs).
+void plan_items(const bsa_cross_s* c, int per, int splits, bsa::CrossTiles* t) {
+  t->items = c->B * c->heads_kv * per * splits;
+  t->div_items = make_fastdiv((uint32_t)per);
+  t->div_splits = make_fastdiv((uint32_t)splits);
+}
+
+// The schedules of the tensor-core kernels.
+void plan_tc(bsa_cross_s* c) {
+  const long long bh = (long long)c->B * c->heads_kv;
   const int key_tiles = (c->n_kv + 127) / 128;
+  plan_tiles(c, false, &c->fwd);
   // Two tiles per item over the same keys, or one tile over two runs of keys
   // (always merged): whichever the estimate says ends first, a round of both
   // streams being the unit and partials and merge costing about three rounds.
+  const int tiles = c->fwd.tiles;
   double pair, dual;
   const int len = split_units(bh * ((tiles + 1) / 2), key_tiles, kSms, 3.0, &pair);
   const int half = split_units(bh * tiles, (key_tiles + 1) / 2, kSms, 0.0, &dual);
-  t.shared = key_tiles == 1 || pair <= dual + 3.0;
-  c->fwd_len = t.shared ? len : 2 * half;
+  c->fwd.shared = key_tiles == 1 || pair <= dual + 3.0;
+  c->fwd_len = c->fwd.shared ? len : 2 * half;
   const int splits = (key_tiles + c->fwd_len - 1) / c->fwd_len;
-  c->fwd_splits = t.shared ? splits : 2 * splits;
-  const int per = (int)(t.shared ? (tiles + 1) / 2 : tiles);
-  t.items = (int)(bh * per * splits);
-  t.ctas = kSms;
-  t.div_items = make_fastdiv((uint32_t)per);
-  t.div_splits = make_fastdiv((uint32_t)splits);
-  t.div_hkv = make_fastdiv((uint32_t)c->heads_kv);
-  t.div_tok = make_fastdiv((uint32_t)((c->n_q + t.tokens - 1) / t.tokens));
-  t.div_pack = make_fastdiv((uint32_t)t.pack);
+  c->fwd_splits = c->fwd.shared ? splits : 2 * splits;
+  plan_items(c, c->fwd.shared ? (tiles + 1) / 2 : tiles, splits, &c->fwd);
+  plan_tiles(c, true, &c->bwd);
+  c->bwd.shared = 1;
+  const int pairs = (c->bwd.tiles + 1) / 2;
+  c->dq_len = split_units(bh * pairs, key_tiles, kSms, 2.0);
+  c->dq_splits = (key_tiles + c->dq_len - 1) / c->dq_len;
+  plan_items(c, pairs, c->dq_splits, &c->bwd);
+  c->dkv_len = split_units(bh * key_tiles, c->bwd.tiles, kSms, 2.0);
+  c->dkv_splits = (c->bwd.tiles + c->dkv_len - 1) / c->dkv_len;
 }
 
 // Map (d, head, token, batch) of a [B, n, heads, D] bf16 view with a box of 64
@@ -105,11 +124,16 @@ size_t forward_bytes(const bsa_cross_s* p) {
          round256((size_t)p->fwd_splits * rows_of(p) * sizeof(float2));
 }
 
+// Backward workspace: the row sums (with lse in the query tiles' order on the
+// tensor cores), then the partials of dQ, whose place those of dK and dV take.
+size_t stats_bytes(const bsa_cross_s* p) {
+  return p->dtype == BSA_BF16 ? round256((size_t)p->B * p->heads_kv * p->bwd.tiles * 256 * sizeof(float))
+                              : round256(rows_of(p) * sizeof(float));
+}
 size_t backward_bytes(const bsa_cross_s* p) {
-  size_t n = round256(rows_of(p) * sizeof(float));
-  if (p->dkv_splits > 1)
-    n += round256((size_t)p->dkv_splits * 2 * p->B * p->heads_kv * p->n_kv * p->D * sizeof(float));
-  return n;
+  const size_t q = p->dq_splits > 1 ? (size_t)p->dq_splits * rows_of(p) : 0;
+  const size_t kv = p->dkv_splits > 1 ? (size_t)p->dkv_splits * 2 * p->B * p->heads_kv * p->n_kv : 0;
+  return stats_bytes(p) + round256((q > kv ? q : kv) * p->D * sizeof(float));
 }
 
 bsa_status check_cross(const bsa_cross_s* p) {
@@ -152,6 +176,23 @@ bsa_status fill(const bsa_cross_s* p, const bsa_view_t* q, const bsa_view_t* k, 
   return BSA_OK;
 }
 
+// The maps of q, k, v (and d_o) for a schedule, whose steps and limits it sets.
+bsa_status make_maps(const bsa_cross_s* p, const bsa::CrossArgs& a, bool backward, bsa::CrossMaps* m,
+                     bsa::CrossTiles* t) {
+  std::memset(m, 0, sizeof(*m));
+  bsa_status s;
+  if ((s = make_map(&m->q, a.q, p->B, p->n_q, p->heads, p->D, t->pack, t->tokens, &t->step_qb, &t->step_qh)) != BSA_OK ||
+      (s = make_map(&m->k, a.k, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t->step_kb, &t->step_kh)) != BSA_OK ||
+      (s = make_map(&m->v, a.v, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t->step_vb, &t->step_vh)) != BSA_OK)
+    return s;
+  if (backward && (s = make_map(&m->d_o, a.d_o, p->B, p->n_q, p->heads, p->D, t->pack, t->tokens, &t->step_ob,
+                                &t->step_oh)) != BSA_OK)
+    return s;
+  t->wait_limit = p->wait_limit;
+  t->hold_load = p->hold_load;
+  return BSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -187,13 +228,15 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   const long long kT = bsa::kCrossSimtTile, bh = (long long)batch * heads_kv;
   const long long row_tiles = ((long long)(heads / heads_kv) * n_q + kT - 1) / kT, key_tiles = (n_kv + kT - 1) / kT;
   if (dtype == BSA_BF16) {
-    plan_forward(&c);
+    plan_tc(&c);
   } else {
     c.fwd_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 1.0);
     c.fwd_splits = (int)((key_tiles + c.fwd_len - 1) / c.fwd_len);
+    c.dq_len = split_units(row_tiles * bh, key_tiles, kSms, 1.0);
+    c.dq_splits = (int)((key_tiles + c.dq_len - 1) / c.dq_len);
+    c.dkv_len = split_units(key_tiles * bh, row_tiles, kSms, 1.0);
+    c.dkv_splits = (int)((row_tiles + c.dkv_len - 1) / c.dkv_len);
   }
-  c.dkv_len = split_units(key_tiles * bh, row_tiles, kSms, 1.0);
-  c.dkv_splits = (int)((row_tiles + c.dkv_len - 1) / c.dkv_len);
   cudaError_t e = cudaGetDevice(&c.device);
   if (e != cudaSuccess) return cuda_fail(e);
   if ((e = cudaMalloc(&c.d_status, sizeof(int32_t))) != cudaSuccess) return cuda_fail(e);
@@ -245,17 +288,11 @@ bsa_status bsa_cross_attention(bsa_cross_t p, const bsa_view_t* q, const bsa_vie
   cudaError_t e;
   if (is_bf16) {
     bsa::CrossMaps maps;
-    std::memset(&maps, 0, sizeof(maps));
     bsa::CrossTiles t = p->fwd;
-    if ((s = make_map(&maps.q, a.q, p->B, p->n_q, p->heads, p->D, t.pack, t.tokens, &t.step_qb, &t.step_qh)) != BSA_OK ||
-        (s = make_map(&maps.k, a.k, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t.step_kb, &t.step_kh)) != BSA_OK ||
-        (s = make_map(&maps.v, a.v, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t.step_vb, &t.step_vh)) != BSA_OK)
-      return s;
-    t.wait_limit = p->wait_limit;
-    t.hold_load = p->hold_load;
+    if ((s = make_maps(p, a, false, &maps, &t)) != BSA_OK) return s;
     e = bsa::launch_cross_tc_forward(a, t, maps, p->D, st);
   } else {
-    e = bsa::launch_cross_simt_forward(a, p->D, is_bf16, st);
+    e = bsa::launch_cross_simt_forward(a, p->D, st);
   }
   if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_merge(a, p->D, is_bf16, st);
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
@@ -279,16 +316,26 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
   if (a.dq.p == a.dk.p || a.dq.p == a.dv.p || a.dk.p == a.dv.p)
     return fail(BSA_ERR_INVALID_ARG, "dq, dk and dv are the same memory");
   if ((s = check_ws(ws, ws_bytes, backward_bytes(p))) != BSA_OK) return s;
-  a.lse = const_cast<float*>(lse);
-  a.delta = static_cast<float*>(ws);
-  a.part_kv = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(rows_of(p) * sizeof(float)));
-  cudaStream_t st = (cudaStream_t)stream;
+  if (p->n_q > 1 && a.d_o.n == 0)
+    return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no view that repeats its tokens (token stride 0)");
   const bool is_bf16 = p->dtype == BSA_BF16;
-  cudaError_t e = bsa::launch_cross_delta(a, p->D, is_bf16, st);
-  if (e == cudaSuccess) e = bsa::launch_cross_simt_dq(a, p->D, is_bf16, st);
+  a.lse = const_cast<float*>(lse);
+  a.delta = a.stats = static_cast<float*>(ws);
+  a.part_o = a.part_kv = reinterpret_cast<float*>(static_cast<char*>(ws) + stats_bytes(p));
+  bsa::CrossMaps maps;
+  bsa::CrossTiles t = p->bwd;
+  if (is_bf16 && (s = make_maps(p, a, true, &maps, &t)) != BSA_OK) return s;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = is_bf16 ? bsa::launch_cross_stats(a, t, p->D, st) : bsa::launch_cross_delta(a, p->D, st);
+  a.splits = p->dq_splits;
+  a.split_len = p->dq_len;
+  if (e == cudaSuccess)
+    e = is_bf16 ? bsa::launch_cross_tc_dq(a, t, maps, p->D, st) : bsa::launch_cross_simt_dq(a, p->D, st);
+  if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_sum_q(a, p->D, is_bf16, st);
   a.splits = p->dkv_splits;
   a.split_len = p->dkv_len;
-  if (e == cudaSuccess) e = bsa::launch_cross_simt_dkv(a, p->D, is_bf16, st);
+  if (e == cudaSuccess)
+    e = is_bf16 ? bsa::launch_cross_tc_dkv(a, t, maps, p->D, st) : bsa::launch_cross_simt_dkv(a, p->D, st);
   if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_reduce_kv(a, p->D, is_bf16, st);
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
 }

@@ -5,14 +5,9 @@
 namespace bsa {
 namespace {
 
-template <typename T> __device__ __forceinline__ float4 in4(const T* p);
-template <> __device__ __forceinline__ float4 in4<float>(const float* p) {
+
+__device__ __forceinline__ float4 in4(const float* p) {
   return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <> __device__ __forceinline__ float4 in4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
 }
 __device__ __forceinline__ void out4(float* d, float4 x) { *reinterpret_cast<float4*>(d) = x; }
 __device__ __forceinline__ void out4(__nv_bfloat16* d, float4 x) {
@@ -59,7 +54,7 @@ __global__ void __launch_bounds__(256) cross_merge(CrossArgs a) {
 
 // A group of D / 4 threads per (token, head) row; neighbouring groups take
 // neighbouring heads of a token.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) cross_delta(CrossArgs a) {
   constexpr int G = D / 4;
   const long long rows = cross_rows(a), id = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
@@ -71,13 +66,30 @@ __global__ void __launch_bounds__(256) cross_delta(CrossArgs a) {
     b = (int)(bn / a.n_q);
     n = (int)(bn - (long long)b * a.n_q);
     const int c = (threadIdx.x % G) * 4;
-    const float4 x = in4(reinterpret_cast<const T*>(a.o.p) + b * a.o.b + n * a.o.n + h * a.o.h + c);
-    const float4 y = in4(reinterpret_cast<const T*>(a.d_o.p) + b * a.d_o.b + n * a.d_o.n + h * a.d_o.h + c);
+    const float4 x = in4(reinterpret_cast<const float*>(a.o.p) + b * a.o.b + n * a.o.n + h * a.o.h + c);
+    const float4 y = in4(reinterpret_cast<const float*>(a.d_o.p) + b * a.d_o.b + n * a.d_o.n + h * a.d_o.h + c);
     sum = x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
   }
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (id < rows && threadIdx.x % G == 0) a.delta[((long long)b * a.heads + h) * a.n_q + n] = sum;
+}
+
+// dQ from the partials of the key splits, added in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_sum_q(CrossArgs a) {
+  constexpr int G = D / 4;
+  const long long rows = cross_rows(a), at = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
+  if (at >= rows) return;
+  const int c = (threadIdx.x % G) * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.splits; ++s) {
+    const float4 x = in4(a.part_o + (s * rows + at) * D + c);
+    acc = make_float4(acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w);
+  }
+  int b, h, n;
+  row_of(a, at, b, h, n);
+  out4(reinterpret_cast<T*>(a.dq.p) + b * a.dq.b + n * a.dq.n + h * a.dq.h + c, acc);
 }
 
 // dK and dV from the partials of the row splits, added in order.
@@ -103,7 +115,7 @@ cudaError_t run_aux(int which, const CrossArgs& a, cudaStream_t st) {
   const long long rows = cross_rows(a), keys = (long long)a.B * a.heads_kv * a.n_kv;
   const unsigned row_ctas = (unsigned)((rows + 1024 / D - 1) / (1024 / D));
   if (which == 0) cross_merge<T, D><<<row_ctas, 256, 0, st>>>(a);
-  else if (which == 1) cross_delta<T, D><<<row_ctas, 256, 0, st>>>(a);
+  else if (which == 1) cross_sum_q<T, D><<<row_ctas, 256, 0, st>>>(a);
   else cross_reduce_kv<T, D><<<dim3((unsigned)((keys * (D / 4) + 255) / 256), 2), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
@@ -118,11 +130,17 @@ cudaError_t run_aux(int which, const CrossArgs& a, int D, bool is_bf16, cudaStre
 cudaError_t launch_cross_merge(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
   return run_aux(0, a, D, is_bf16, st);
 }
-cudaError_t launch_cross_delta(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
+cudaError_t launch_cross_sum_q(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
   return run_aux(1, a, D, is_bf16, st);
 }
 cudaError_t launch_cross_reduce_kv(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
   return run_aux(2, a, D, is_bf16, st);
+}
+cudaError_t launch_cross_delta(const CrossArgs& a, int D, cudaStream_t st) {
+  const unsigned ctas = (unsigned)((cross_rows(a) + 1024 / D - 1) / (1024 / D));
+  if (D == 128) cross_delta<128><<<ctas, 256, 0, st>>>(a);
+  else cross_delta<64><<<ctas, 256, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace bsa

@@ -19,44 +19,35 @@ constexpr int kPad = kT + 4;     // row stride of a tile of probabilities
 template <int D> constexpr int row_floats() { return D + 4; }
 
 // Where row r (of one K/V head's rows) of a per-token tensor starts.
-template <typename T>
-__device__ __forceinline__ const T* row_ptr(const CrossArgs& a, const View& v, int b, int hk, long long r) {
+__device__ __forceinline__ float* row_ptr(const CrossArgs& a, const View& v, int b, int hk, long long r) {
   const int g = (int)(r / a.n_q);
   const long long n = r - (long long)g * a.n_q;
-  return reinterpret_cast<const T*>(v.p) + b * v.b + n * v.n + (long long)(hk * a.group + g) * v.h;
+  return reinterpret_cast<float*>(v.p) + b * v.b + n * v.n + (long long)(hk * a.group + g) * v.h;
 }
 
 __device__ __forceinline__ void put4(float* d, const float* s) {
   *reinterpret_cast<float4*>(d) = __ldg(reinterpret_cast<const float4*>(s));
 }
-__device__ __forceinline__ void put4(float* d, const __nv_bfloat16* s) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(s));
-  *reinterpret_cast<float4*>(d) = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                              __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
 __device__ __forceinline__ void out4(float* d, float4 x) { *reinterpret_cast<float4*>(d) = x; }
-__device__ __forceinline__ void out4(__nv_bfloat16* d, float4 x) {
-  *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-}
 
 // Loads rows r0 .. r0 + 63 (zeros from `end` on) of a row tensor.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_rows(float* s, const CrossArgs& a, const View& v, int b, int hk, long long r0,
                                           long long end) {
   for (int i = threadIdx.x; i < kT * (D / 4); i += 256) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     float* d = s + r * row_floats<D>() + c;
-    if (r0 + r < end) put4(d, row_ptr<T>(a, v, b, hk, r0 + r) + c);
+    if (r0 + r < end) put4(d, row_ptr(a, v, b, hk, r0 + r) + c);
     else *reinterpret_cast<float4*>(d) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
 // Loads keys j0 .. j0 + 63 of K or V; keys that are not attended read as zeros
 // whatever they hold.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_keys(float* s, const CrossArgs& a, const View& v, int b, int hk, int j0,
                                           const uint8_t* seen) {
-  const T* base = reinterpret_cast<const T*>(v.p) + b * v.b + hk * v.h;
+  const float* base = reinterpret_cast<const float*>(v.p) + b * v.b + hk * v.h;
   for (int i = threadIdx.x; i < kT * (D / 4); i += 256) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     float* d = s + r * row_floats<D>() + c;
@@ -147,7 +138,7 @@ __device__ __forceinline__ void clear(float2 (&acc)[4][D / 32]) {
 
 // Online softmax over the key tiles of one split; the probabilities replace K
 // in shared memory for the product with V.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256, 2) cross_simt_forward(CrossArgs a) {
   extern __shared__ float4 smem4[];
   float* sQ = reinterpret_cast<float*>(smem4);
@@ -161,7 +152,7 @@ __global__ void __launch_bounds__(256, 2) cross_simt_forward(CrossArgs a) {
   const long long r0 = (long long)(blockIdx.x % per) * kT;
   const int keys = cross_keys(a, b), tiles = (keys + kT - 1) / kT;
   const int t0 = blockIdx.y * a.split_len, t1 = min(tiles, t0 + a.split_len);
-  load_rows<T, D>(sQ, a, a.q, b, hk, r0, rows);
+  load_rows<D>(sQ, a, a.q, b, hk, r0, rows);
   float m[4], l[4];
   float2 acc[4][D / 32];
   clear<D>(acc);
@@ -171,8 +162,8 @@ __global__ void __launch_bounds__(256, 2) cross_simt_forward(CrossArgs a) {
     __syncthreads();
     load_seen(seen, a, b, t * kT, keys);
     __syncthreads();
-    load_keys<T, D>(sK, a, a.k, b, hk, t * kT, seen);
-    load_keys<T, D>(sV, a, a.v, b, hk, t * kT, seen);
+    load_keys<D>(sK, a, a.k, b, hk, t * kT, seen);
+    load_keys<D>(sV, a, a.v, b, hk, t * kT, seen);
     __syncthreads();
     float s[4][4];
     dot_tile<D>(sQ, sK, ty, tx, s);
@@ -217,7 +208,7 @@ __global__ void __launch_bounds__(256, 2) cross_simt_forward(CrossArgs a) {
       if (tx == 0) a.part_ml[p] = make_float2(m[i], l[i]);
     } else {
       const float inv = m[i] == -INFINITY ? 0.f : 1.f / l[i];
-      T* d = const_cast<T*>(row_ptr<T>(a, a.o, b, hk, r));
+      float* d = row_ptr(a, a.o, b, hk, r);
 #pragma unroll
       for (int q = 0; q < D / 64; ++q)
         out4(d + tx * 4 + 64 * q, make_float4(acc[i][2 * q].x * inv, acc[i][2 * q].y * inv,
@@ -240,8 +231,8 @@ __device__ __forceinline__ float lse2_of(const CrossArgs& a, long long at, bool 
   return x == -INFINITY ? INFINITY : x * 1.4426950408889634f;
 }
 
-// dQ of 64 rows, over all key tiles.  dS replaces V in shared memory.
-template <typename T, int D>
+// dQ of 64 rows, over the key tiles of one split.  dS replaces V in shared memory.
+template <int D>
 __global__ void __launch_bounds__(256) cross_simt_dq(CrossArgs a) {
   extern __shared__ float4 smem4[];
   float* sQ = reinterpret_cast<float*>(smem4);
@@ -256,8 +247,8 @@ __global__ void __launch_bounds__(256) cross_simt_dq(CrossArgs a) {
   const long long r0 = (long long)(blockIdx.x % per) * kT;
   const long long at0 = ((long long)b * a.heads + (long long)hk * a.group) * a.n_q;
   const int keys = cross_keys(a, b), tiles = (keys + kT - 1) / kT;
-  load_rows<T, D>(sQ, a, a.q, b, hk, r0, rows);
-  load_rows<T, D>(sO, a, a.d_o, b, hk, r0, rows);
+  load_rows<D>(sQ, a, a.q, b, hk, r0, rows);
+  load_rows<D>(sO, a, a.d_o, b, hk, r0, rows);
   float lse2[4], delta[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -267,12 +258,13 @@ __global__ void __launch_bounds__(256) cross_simt_dq(CrossArgs a) {
   }
   float2 acc[4][D / 32];
   clear<D>(acc);
-  for (int t = 0; t < tiles; ++t) {
+  const int t0 = blockIdx.y * a.split_len, t1 = min(tiles, t0 + a.split_len);
+  for (int t = t0; t < t1; ++t) {
     __syncthreads();
     load_seen(seen, a, b, t * kT, keys);
     __syncthreads();
-    load_keys<T, D>(sK, a, a.k, b, hk, t * kT, seen);
-    load_keys<T, D>(sV, a, a.v, b, hk, t * kT, seen);
+    load_keys<D>(sK, a, a.k, b, hk, t * kT, seen);
+    load_keys<D>(sV, a, a.v, b, hk, t * kT, seen);
     __syncthreads();
     float s[4][4], dp[4][4];
     dot_tile<D>(sQ, sK, ty, tx, s);
@@ -292,7 +284,7 @@ __global__ void __launch_bounds__(256) cross_simt_dq(CrossArgs a) {
   for (int i = 0; i < 4; ++i) {
     const long long r = r0 + ty * 4 + i;
     if (r >= rows) continue;
-    T* d = const_cast<T*>(row_ptr<T>(a, a.dq, b, hk, r));
+    float* d = a.splits > 1 ? a.part_o + (blockIdx.y * cross_rows(a) + at0 + r) * D : row_ptr(a, a.dq, b, hk, r);
 #pragma unroll
     for (int q = 0; q < D / 64; ++q)
       out4(d + tx * 4 + 64 * q, make_float4(acc[i][2 * q].x * a.scale, acc[i][2 * q].y * a.scale,
@@ -301,7 +293,7 @@ __global__ void __launch_bounds__(256) cross_simt_dq(CrossArgs a) {
 }
 
 // dK and dV of 64 keys, over the row tiles of one split.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) cross_simt_dkv(CrossArgs a) {
   extern __shared__ float4 smem4[];
   float* sK = reinterpret_cast<float*>(smem4);
@@ -324,15 +316,15 @@ __global__ void __launch_bounds__(256) cross_simt_dkv(CrossArgs a) {
   if (j0 >= keys) t1 = t0;      // no key of this tile is attended
   load_seen(seen, a, b, j0, keys);
   __syncthreads();
-  load_keys<T, D>(sK, a, a.k, b, hk, j0, seen);
-  load_keys<T, D>(sV, a, a.v, b, hk, j0, seen);
+  load_keys<D>(sK, a, a.k, b, hk, j0, seen);
+  load_keys<D>(sV, a, a.v, b, hk, j0, seen);
   float2 dk[4][D / 32], dv[4][D / 32];
   clear<D>(dk);
   clear<D>(dv);
   for (long long t = t0; t < t1; ++t) {
     __syncthreads();
-    load_rows<T, D>(sQ, a, a.q, b, hk, t * kT, rows);
-    load_rows<T, D>(sO, a, a.d_o, b, hk, t * kT, rows);
+    load_rows<D>(sQ, a, a.q, b, hk, t * kT, rows);
+    load_rows<D>(sO, a, a.d_o, b, hk, t * kT, rows);
     if (threadIdx.x < kT) {
       const long long r = t * kT + threadIdx.x;
       s_lse2[threadIdx.x] = lse2_of(a, at0 + r, r < rows);
@@ -371,14 +363,14 @@ __global__ void __launch_bounds__(256) cross_simt_dkv(CrossArgs a) {
         out4(a.part_kv + ((2ll * blockIdx.y) * all + at) * D + c, gk);
         out4(a.part_kv + ((2ll * blockIdx.y + 1) * all + at) * D + c, gv);
       } else {
-        out4(reinterpret_cast<T*>(a.dk.p) + b * a.dk.b + j * a.dk.n + hk * a.dk.h + c, gk);
-        out4(reinterpret_cast<T*>(a.dv.p) + b * a.dv.b + j * a.dv.n + hk * a.dv.h + c, gv);
+        out4(reinterpret_cast<float*>(a.dk.p) + b * a.dk.b + j * a.dk.n + hk * a.dk.h + c, gk);
+        out4(reinterpret_cast<float*>(a.dv.p) + b * a.dv.b + j * a.dv.n + hk * a.dv.h + c, gv);
       }
     }
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run_simt(int which, const CrossArgs& a, cudaStream_t st) {
   const int tile = kT * row_floats<D>() * (int)sizeof(float);
   const long long rows = (long long)a.group * a.n_q;
@@ -387,15 +379,15 @@ cudaError_t run_simt(int which, const CrossArgs& a, cudaStream_t st) {
   int smem;
   dim3 grid;
   if (which == 0) {
-    kernel = cross_simt_forward<T, D>;
+    kernel = cross_simt_forward<D>;
     smem = 3 * tile;
     grid = dim3(row_tiles * a.B * a.heads_kv, a.splits);
   } else if (which == 1) {
-    kernel = cross_simt_dq<T, D>;
+    kernel = cross_simt_dq<D>;
     smem = 4 * tile;
-    grid = dim3(row_tiles * a.B * a.heads_kv);
+    grid = dim3(row_tiles * a.B * a.heads_kv, a.splits);
   } else {
-    kernel = cross_simt_dkv<T, D>;
+    kernel = cross_simt_dkv<D>;
     smem = 4 * tile + 2 * kT * kPad * (int)sizeof(float);
     grid = dim3(key_tiles * a.B * a.heads_kv, a.splits);
   }
@@ -405,21 +397,14 @@ cudaError_t run_simt(int which, const CrossArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t run_simt(int which, const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
-  if (is_bf16) return D == 128 ? run_simt<__nv_bfloat16, 128>(which, a, st) : run_simt<__nv_bfloat16, 64>(which, a, st);
-  return D == 128 ? run_simt<float, 128>(which, a, st) : run_simt<float, 64>(which, a, st);
+cudaError_t run_simt(int which, const CrossArgs& a, int D, cudaStream_t st) {
+  return D == 128 ? run_simt<128>(which, a, st) : run_simt<64>(which, a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
-  return run_simt(0, a, D, is_bf16, st);
-}
-cudaError_t launch_cross_simt_dq(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
-  return run_simt(1, a, D, is_bf16, st);
-}
-cudaError_t launch_cross_simt_dkv(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
-  return run_simt(2, a, D, is_bf16, st);
-}
+cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, cudaStream_t st) { return run_simt(0, a, D, st); }
+cudaError_t launch_cross_simt_dq(const CrossArgs& a, int D, cudaStream_t st) { return run_simt(1, a, D, st); }
+cudaError_t launch_cross_simt_dkv(const CrossArgs& a, int D, cudaStream_t st) { return run_simt(2, a, D, st); }
 
 }  // namespace bsa

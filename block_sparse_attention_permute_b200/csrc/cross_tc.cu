@@ -16,16 +16,12 @@
 // tile, the tensor core works for the other one, and the next tile's S is
 // formed during the epilogue.  A commit after S_x(s) covers every earlier MMA,
 // so a softmax warp that sees it may rescale O_x.
-#include "cross.cuh"
+#include "cross_tc.cuh"
 
 namespace bsa {
 namespace {
 
-constexpr int kThreads = 384;
-// Registers: the launch gives kRegsLaunch to each thread; the load/MMA
-// warpgroup then drops to kRegsSmall and the softmax warpgroups rise.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsSmall = 72;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsSmall <= kThreads * kRegsLaunch, "register split");
+using Regs = RegSplit<216, 72>;
 constexpr float kRescale = 8.0f;   // log2 units by which a row's maximum may lag
 
 template <int HD>
@@ -41,62 +37,6 @@ struct Layout {
   static constexpr int kTmemSlot = kBars + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kAlloc = kAbort + 4 + 1024;   // room to align the base to 1024
-};
-
-// What an item gives to one stream.
-struct Work {
-  int b, hk, h0, tok0;   // batch element, K/V head, first head and token of the query tile
-  int kt, n;             // key tiles kt .. kt + n - 1
-  int split;             // index of its partial
-  bool real;             // false: the padding tile of an odd pair
-};
-
-__device__ __forceinline__ Work decode(const CrossArgs& a, const CrossTiles& t, int it, int x) {
-  Work w;
-  const int rest = (int)fdiv((uint32_t)it, t.div_items), i = it - rest * (int)t.div_items.d;
-  const int bh = (int)fdiv((uint32_t)rest, t.div_splits);
-  w.split = rest - bh * (int)t.div_splits.d;
-  w.b = (int)fdiv((uint32_t)bh, t.div_hkv);
-  w.hk = bh - w.b * a.heads_kv;
-  const int tile = t.shared ? 2 * i + x : i;
-  const int sg = (int)fdiv((uint32_t)tile, t.div_tok), tt = tile - sg * (int)t.div_tok.d;
-  w.real = tile < t.tiles;
-  w.h0 = w.hk * a.group + sg * t.pack;
-  w.tok0 = tt * t.tokens;
-  const int tiles = (cross_keys(a, w.b) + 127) >> 7;
-  w.kt = w.split * a.split_len;
-  w.n = max(0, min(a.split_len, tiles - w.kt));
-  if (!t.shared) {
-    const int first = (w.n + 1) >> 1;
-    w.split = 2 * w.split + x;
-    if (x) w.kt += first;
-    w.n = x ? w.n - first : first;
-  }
-  return w;
-}
-
-// Walks the steps of one stream over the CTA's items.
-struct Cursor {
-  int it, s;
-  Work w;
-  __device__ __forceinline__ bool valid(const CrossTiles& t) const { return it < t.items; }
-  __device__ __forceinline__ void find(const CrossArgs& a, const CrossTiles& t, int x) {
-    for (; it < t.items; it += gridDim.x) {
-      w = decode(a, t, it, x);
-      if (w.n > 0) break;
-    }
-    s = 0;
-  }
-  __device__ __forceinline__ void start(const CrossArgs& a, const CrossTiles& t, int x) {
-    it = blockIdx.x;
-    find(a, t, x);
-  }
-  __device__ __forceinline__ void advance(const CrossArgs& a, const CrossTiles& t, int x) {
-    if (++s == w.n) {
-      it += gridDim.x;
-      find(a, t, x);
-    }
-  }
 };
 
 // f(kind, x, cursor) for every event of the CTA in issue order; kind 0 is
@@ -119,19 +59,6 @@ __device__ __forceinline__ bool for_each_event(const CrossArgs& a, const CrossTi
     }
   }
   return true;
-}
-
-// Bit c of word w: key j0 + 32 w + c is attended (whole warp).
-__device__ __forceinline__ uint4 seen_bits(const CrossArgs& a, int b, int j0, int keys, int lane) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = j0 + 32 * i + lane;
-    bool s = j < keys;
-    if (s && a.key_mask) s = __ldg(a.key_mask + (long long)b * a.n_kv + j) != 0;
-    w[i] = __ballot_sync(0xffffffffu, s);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int HD>
@@ -162,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kTmemSlot);
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSmall));
+    Regs::small();
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------------------ loads
       int pos = 0, nq[2] = {0, 0};
@@ -224,20 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // even times 0: those rows become zeros (rows past n_kv are).
             const int keys = cross_keys(a, w.b), j0 = (w.kt + c.s) * 128;
             if (a.key_mask != nullptr || j0 + 128 > keys) {
-              const uint4 m = seen_bits(a, w.b, j0, keys, lane);
-              const uint32_t m4[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (!((m4[i] >> lane) & 1u)) {
-                  uint8_t* row = sm + L::kRing + slot * L::kTile + (32 * i + lane) * 128;
-#pragma unroll
-                  for (int p = 0; p < HD / 64; ++p)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                      reinterpret_cast<uint4*>(row + p * L::kPanel)[e] = make_uint4(0u, 0u, 0u, 0u);
-                }
-              fence_proxy_async_smem();
-              __syncwarp();
+              zero_hidden_rows<HD>(sm + L::kRing + slot * L::kTile, seen_bits(a, w.b, j0, keys, lane), lane);
             }
           }
         }
@@ -276,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    Regs::rows();
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;    // stream, query row of the tile (TMEM lane)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128u * x + lane_off, tO = tmem + 256u + 128u * x + lane_off;
@@ -429,13 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int HD>
 cudaError_t launch(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, cudaStream_t st) {
-  // The register split assumes the launch gives every thread kRegsLaunch
-  // registers; a build where that is not so is refused.
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, cross_tc_forward<HD>);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(cross_tc_forward<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::kAlloc);
+  const cudaError_t e = prepare_kernel(cross_tc_forward<HD>, Layout<HD>::kAlloc);
   if (e != cudaSuccess) return e;
   cross_tc_forward<HD><<<t.items < t.ctas ? t.items : t.ctas, kThreads, Layout<HD>::kAlloc, st>>>(a, t, m);
   return cudaGetLastError();
