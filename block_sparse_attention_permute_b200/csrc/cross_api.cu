@@ -31,15 +31,16 @@ bsa_status cuda_fail(cudaError_t e) { return fail(BSA_ERR_CUDA, cudaGetErrorStri
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Splits `units` of work of each of `ctas` CTAs over several CTAs when that
-// shortens the call: `slots` CTAs run at a time, and a split call costs its CTAs
-// about `extra` units more, to write the partials and to merge them.  Returns
-// the units per split, *cost its estimate.
-int split_units(long long ctas, long long units, int slots, double extra, double* cost = nullptr) {
+// shortens the call: `slots` CTAs run at a time, each costs about `start` units
+// beside its work (its loads before the first product, its stores after the
+// last), and a split call about `extra` units more, for writing and merging the
+// partials.  Returns the units per split, *cost its estimate.
+int split_units(long long ctas, long long units, int slots, double start, double extra, double* cost = nullptr) {
   long long len = units;
-  double best = (double)((ctas + slots - 1) / slots) * units;
+  double best = (double)((ctas + slots - 1) / slots) * (units + start);
   for (int s = 2; s <= 128 && s <= units; ++s) {
     const long long l = (units + s - 1) / s, n = (units + l - 1) / l;
-    const double c = (double)((ctas * n + slots - 1) / slots) * l + extra;
+    const double c = (double)((ctas * n + slots - 1) / slots) * (l + start) + extra;
     if (c < best) best = c, len = l;
   }
   if (cost) *cost = best;
@@ -84,8 +85,8 @@ void plan_tc(bsa_cross_s* c) {
   // streams being the unit and partials and merge costing about three rounds.
   const int tiles = c->fwd.tiles;
   double pair, dual;
-  const int len = split_units(bh * ((tiles + 1) / 2), key_tiles, kSms, 3.0, &pair);
-  const int half = split_units(bh * tiles, (key_tiles + 1) / 2, kSms, 0.0, &dual);
+  const int len = split_units(bh * ((tiles + 1) / 2), key_tiles, kSms, 1.0, 3.0, &pair);
+  const int half = split_units(bh * tiles, (key_tiles + 1) / 2, kSms, 1.0, 0.0, &dual);
   c->fwd.shared = key_tiles == 1 || pair <= dual + 3.0;
   c->fwd_len = c->fwd.shared ? len : 2 * half;
   const int splits = (key_tiles + c->fwd_len - 1) / c->fwd_len;
@@ -94,10 +95,10 @@ void plan_tc(bsa_cross_s* c) {
   plan_tiles(c, true, &c->bwd);
   c->bwd.shared = 1;
   const int pairs = (c->bwd.tiles + 1) / 2;
-  c->dq_len = split_units(bh * pairs, key_tiles, kSms, 2.0);
+  c->dq_len = split_units(bh * pairs, key_tiles, kSms, 1.0, 2.0);
   c->dq_splits = (key_tiles + c->dq_len - 1) / c->dq_len;
   plan_items(c, pairs, c->dq_splits, &c->bwd);
-  c->dkv_len = split_units(bh * key_tiles, c->bwd.tiles, kSms, 2.0);
+  c->dkv_len = split_units(bh * key_tiles, c->bwd.tiles, kSms, 3.0, 2.0);
   c->dkv_splits = (c->bwd.tiles + c->dkv_len - 1) / c->dkv_len;
 }
 
@@ -230,11 +231,11 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   if (dtype == BSA_BF16) {
     plan_tc(&c);
   } else {
-    c.fwd_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 1.0);
+    c.fwd_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 0.5, 1.0);
     c.fwd_splits = (int)((key_tiles + c.fwd_len - 1) / c.fwd_len);
-    c.dq_len = split_units(row_tiles * bh, key_tiles, kSms, 1.0);
+    c.dq_len = split_units(row_tiles * bh, key_tiles, kSms, 1.0, 1.0);
     c.dq_splits = (int)((key_tiles + c.dq_len - 1) / c.dq_len);
-    c.dkv_len = split_units(key_tiles * bh, row_tiles, kSms, 1.0);
+    c.dkv_len = split_units(key_tiles * bh, row_tiles, kSms, 1.0, 1.0);
     c.dkv_splits = (int)((row_tiles + c.dkv_len - 1) / c.dkv_len);
   }
   cudaError_t e = cudaGetDevice(&c.device);

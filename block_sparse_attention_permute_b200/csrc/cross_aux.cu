@@ -22,34 +22,59 @@ __device__ __forceinline__ void row_of(const CrossArgs& a, long long at, int& b,
   h = (int)(bh - (long long)b * a.heads);
 }
 
-// A group of D / 4 threads per row.  With partials (O_s, m_s, l_s) of the key
-// splits: M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s, and
-// lse = ln 2 (M + log2 sum w_s l_s).  Splits are taken in order.
+// One warp per row.  With partials (O_s, m_s, l_s) of the key splits:
+// M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s, and
+// lse = ln 2 (M + log2 sum w_s l_s).  The lanes first share the splits, then
+// the columns (D = 64: half a warp takes every other split); eight partial rows
+// are in flight, since few rows leave latency as the bound.  Every sum has a
+// fixed order.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_merge(CrossArgs a) {
-  constexpr int G = D / 4;
-  const long long rows = cross_rows(a), at = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
+  constexpr int kHalves = 128 / D;
+  const long long rows = cross_rows(a), at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (at >= rows) return;
-  const int c = (threadIdx.x % G) * 4;
+  const int lane = threadIdx.x & 31, c = (lane % (D / 4)) * 4, first = lane / (D / 4);
   float M = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[s * rows + at].x);
+  for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, __ldg(a.part_ml + s * rows + at).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float base = M == -INFINITY ? 0.f : M;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.part_ml[s * rows + at];
-    if (ml.x == -INFINITY) continue;   // no key: its O is not written
-    const float w = exp2f(ml.x - base);
-    const float4 x = in4(a.part_o + (s * rows + at) * D + c);
-    l = fmaf(w, ml.y, l);
-    acc = make_float4(fmaf(w, x.x, acc.x), fmaf(w, x.y, acc.y), fmaf(w, x.z, acc.z), fmaf(w, x.w, acc.w));
+  for (int s = lane; s < a.splits; s += 32) {
+    const float2 ml = __ldg(a.part_ml + s * rows + at);
+    l = fmaf(exp2f(ml.x - base), ml.y, l);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = first; s0 < a.splits; s0 += 8 * kHalves) {
+    float4 x[8];
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int s = s0 + u * kHalves;
+      // a split without keys (m = -inf, w = 0) has not written its O
+      w[u] = s < a.splits ? exp2f(__ldg(a.part_ml + s * rows + at).x - base) : 0.f;
+      x[u] = w[u] != 0.f ? in4(a.part_o + (s * rows + at) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      acc = make_float4(fmaf(w[u], x[u].x, acc.x), fmaf(w[u], x[u].y, acc.y), fmaf(w[u], x[u].z, acc.z),
+                        fmaf(w[u], x[u].w, acc.w));
+  }
+  if (kHalves == 2) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / l;
   int b, h, n;
   row_of(a, at, b, h, n);
-  out4(reinterpret_cast<T*>(a.o.p) + b * a.o.b + n * a.o.n + h * a.o.h + c,
-       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (c == 0 && a.lse) a.lse[at] = (M + log2f(l)) * 0.69314718055994531f;
+  if (first == 0)
+    out4(reinterpret_cast<T*>(a.o.p) + b * a.o.b + n * a.o.n + h * a.o.h + c,
+         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (lane == 0 && a.lse) a.lse[at] = (M + log2f(l)) * 0.69314718055994531f;
 }
 
 // A group of D / 4 threads per (token, head) row; neighbouring groups take
@@ -114,7 +139,7 @@ template <typename T, int D>
 cudaError_t run_aux(int which, const CrossArgs& a, cudaStream_t st) {
   const long long rows = cross_rows(a), keys = (long long)a.B * a.heads_kv * a.n_kv;
   const unsigned row_ctas = (unsigned)((rows + 1024 / D - 1) / (1024 / D));
-  if (which == 0) cross_merge<T, D><<<row_ctas, 256, 0, st>>>(a);
+  if (which == 0) cross_merge<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
   else if (which == 1) cross_sum_q<T, D><<<row_ctas, 256, 0, st>>>(a);
   else cross_reduce_kv<T, D><<<dim3((unsigned)((keys * (D / 4) + 255) / 256), 2), 256, 0, st>>>(a);
   return cudaGetLastError();

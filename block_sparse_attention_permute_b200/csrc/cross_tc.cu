@@ -2,7 +2,8 @@
 //
 // One persistent CTA per SM walks over items.  Each CTA runs two streams of
 // 128-row query tiles: warps 0-3 and 4-7 are the softmax of stream 0 and 1 (a
-// query row per thread), warp 8 issues the TMA loads, warp 9 the MMAs.  An item
+// query row per thread), warp 8 issues the TMA loads, warp 9 the MMAs, warps 10
+// and 11 clear V at masked keys.  An item
 // gives each stream a query tile and a run of key tiles; either the streams
 // take two query tiles of one K/V head over the same keys and share every K and
 // V tile in shared memory, or (few query rows) the same query tile over the two
@@ -28,12 +29,14 @@ template <int HD>
 struct Layout {
   static constexpr int kTile = 128 * HD * 2;
   static constexpr int kPanel = 128 * 128;       // 128 rows x 64 columns (one TMA box)
-  static constexpr int kStages = HD == 128 ? 5 : 10;
+  static constexpr int kStages = HD == 128 ? 2 : 4;         // slots of the K ring, and of the V ring
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
-  static constexpr int kBars = kRing + kStages * kTile;
-  static constexpr int kQFull = 0, kQEmpty = 2, kFull = 4, kEmpty = 4 + kStages, kS = 4 + 2 * kStages, kP = kS + 2,
-                       kO = kP + 2, kFinal = kO + 2, kNumBars = kFinal + 1;
+  static constexpr int kStore = kRing + 2 * kStages * kTile; // 4 KB per softmax warp
+  static constexpr int kBars = kStore + 8 * 4096;
+  static constexpr int kQFull = 0, kQEmpty = 2, kFull = 4, kEmpty = kFull + 2 * kStages,
+                       kClean = kEmpty + 2 * kStages, kS = kClean + kStages, kP = kS + 2, kO = kP + 2,
+                       kFinal = kO + 2, kNumBars = kFinal + 1;
   static constexpr int kTmemSlot = kBars + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kAlloc = kAbort + 4 + 1024;   // room to align the base to 1024
@@ -73,9 +76,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kAbort);
   const long long lim = t.wait_limit > 0 ? t.wait_limit : kWaitLimitDefault;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool cleaning = a.key_mask != nullptr || a.kv_len != nullptr;
 
   if (threadIdx.x == 0) {
-    for (int x = 0; x < L::kNumBars; ++x) mbar_init(bar(x), (x == L::kP || x == L::kP + 1) ? 128u : 1u);
+    for (int x = 0; x < L::kNumBars; ++x)
+      mbar_init(bar(x), x == L::kP || x == L::kP + 1 ? 128u : x >= L::kClean && x < L::kClean + L::kStages ? 2u : 1u);
     *abort = 0;
     fence_mbar_init();
   }
@@ -92,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Regs::small();
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------------------ loads
-      int pos = 0, nq[2] = {0, 0};
+      int pos[2] = {0, 0}, nq[2] = {0, 0};
       const uint32_t q_bytes = (uint32_t)(t.pack * t.tokens * HD * 2);
       for_each_event(a, t, [&](int kind, int x, const Cursor& c) -> bool {
         const Work& w = c.w;
@@ -108,9 +113,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nq[x];
         }
         if (t.shared && x == 1) return true;
-        if (pos + 1 == t.hold_load && blockIdx.x == 0) return false;   // test hook: a copy that never lands
-        const int slot = pos % L::kStages;
-        if (pos >= L::kStages && !mbar_wait(bar(L::kEmpty + slot), (pos / L::kStages - 1) & 1, abort, lim)) return false;
+        if (pos[0] + pos[1] + 1 == t.hold_load && blockIdx.x == 0) return false;   // test hook: a copy that never lands
+        const int use = pos[kind] / L::kStages, slot = kind * L::kStages + pos[kind] % L::kStages;
+        if (use > 0 && !mbar_wait(bar(L::kEmpty + slot), (use - 1) & 1, abort, lim)) return false;
         mbar_arrive_expect_tx(bar(L::kFull + slot), L::kTile);
         const CUtensorMap* map = kind ? &maps.v : &maps.k;
         const int hc = w.hk * (kind ? t.step_vh : t.step_kh), bc = w.b * (kind ? t.step_vb : t.step_kb);
@@ -118,42 +123,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int p = 0; p < HD / 64; ++p)
           tma_load_4d(sb + L::kRing + slot * L::kTile + p * L::kPanel, map, 64 * p, hc, (w.kt + c.s) * 128, bc,
                       bar(L::kFull + slot));
-        ++pos;
+        ++pos[kind];
         return true;
       });
       // No copy is left in flight, also after an abort: issued copies land.
       for (int x = 0; x < 2; ++x)
         if (nq[x] > 0) mbar_wait_drain(bar(L::kQFull + x), (nq[x] - 1) & 1, lim);
-      for (int p = pos > L::kStages ? pos - L::kStages : 0; p < pos; ++p)
-        mbar_wait_drain(bar(L::kFull + p % L::kStages), (p / L::kStages) & 1, lim);
+      for (int y = 0; y < 2; ++y)
+        for (int p = pos[y] > L::kStages ? pos[y] - L::kStages : 0; p < pos[y]; ++p)
+          mbar_wait_drain(bar(L::kFull + y * L::kStages + p % L::kStages), (p / L::kStages) & 1, lim);
     } else if (warp == 9) {
       // ------------------------------------------------------------ MMAs (the whole warp waits, lane 0 issues)
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0), idesc_o = idesc_bf16_f32(128, HD, 0, 1);
-      int pos = 0, kept[2] = {0, 0}, nq[2] = {0, 0}, np[2] = {0, 0};
+      int pos[2] = {0, 0}, kept[2] = {0, 0}, nq[2] = {0, 0}, np[2] = {0, 0};
       auto wait = [&](uint32_t b, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(b, parity, abort, lim)) != 0;
       };
       for_each_event(a, t, [&](int kind, int x, const Cursor& c) -> bool {
         const Work& w = c.w;
         const bool own = !(t.shared && x == 1);      // else: the slot stream 0 took
-        const int slot = own ? pos % L::kStages : kept[kind];
+        const int slot = own ? kind * L::kStages + pos[kind] % L::kStages : kept[kind];
         const uint32_t src = sb + L::kRing + slot * L::kTile;
         if (kind == 0 && c.s == 0) {
           if (!wait(bar(L::kQFull + x), nq[x] & 1)) return false;
           ++nq[x];
         }
         if (own) {
-          if (!wait(bar(L::kFull + slot), (pos / L::kStages) & 1)) return false;
-          ++pos;
+          const int ready = kind && cleaning ? L::kClean + slot - L::kStages : L::kFull + slot;
+          if (!wait(bar(ready), (pos[kind] / L::kStages) & 1)) return false;
+          ++pos[kind];
           kept[kind] = slot;
-          if (kind == 1) {
-            // What V holds at keys that are not attended must not enter, not
-            // even times 0: those rows become zeros (rows past n_kv are).
-            const int keys = cross_keys(a, w.b), j0 = (w.kt + c.s) * 128;
-            if (a.key_mask != nullptr || j0 + 128 > keys) {
-              zero_hidden_rows<HD>(sm + L::kRing + slot * L::kTile, seen_bits(a, w.b, j0, keys, lane), lane);
-            }
-          }
         }
         if (kind == 1) {
           if (!wait(bar(L::kP + x), np[x] & 1)) return false;
@@ -187,6 +186,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Every MMA issued is complete before TMEM is released, also after an abort.
       if (lane == 0) tc_commit(bar(L::kFinal));
       mbar_wait_drain(bar(L::kFinal), 0, lim);
+    } else if (warp >= 10 && cleaning) {
+      // ------------------------------------------------------------ cleaning of V
+      // What V holds at keys that are not attended must not enter, not even
+      // times 0: warps 10 and 11 write zeros over those rows (64 rows each)
+      // while the tile waits for its turn.  (Rows past n_kv are zeros.)
+      int pos = 0;
+      for_each_event(a, t, [&](int kind, int x, const Cursor& c) -> bool {
+        if (kind == 0 || (t.shared && x == 1)) return true;
+        const int slot = pos % L::kStages, j0 = (c.w.kt + c.s) * 128, keys = cross_keys(a, c.w.b);
+        const bool hidden = a.key_mask != nullptr || j0 + 128 > keys;
+        uint4 m;
+        if (hidden) m = seen_bits(a, c.w.b, j0, keys, lane);
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kFull + L::kStages + slot), (pos / L::kStages) & 1, abort, lim)))
+          return false;
+        if (hidden) zero_hidden_rows<HD>(sm + L::kRing + (L::kStages + slot) * L::kTile, m, 2 * (warp - 10), lane);
+        if (lane == 0) mbar_arrive(bar(L::kClean + slot));
+        ++pos;
+        return true;
+      });
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -302,29 +320,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row) a.part_ml[p] = make_float2(m_run, l);
       } else {
         const float inv = m_run == -INFINITY ? 0.f : 1.f / l;
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o.p) + w.b * a.o.b + n * a.o.n +
-                                              h * a.o.h);
 #pragma unroll
-        for (int c0 = 0; c0 < HD; c0 += 32) {
-          uint32_t o[32];
+        for (int c0 = 0; c0 < HD; c0 += 64) {
+          uint32_t o[64];
           if (w.n > 0) {
-            TMEM_LD32(tO + c0, o);
-            TMEM_LD_WAIT(o);
+            TMEM_LD32(tO + c0, (o + 0));
+            TMEM_LD32(tO + c0 + 32, (o + 32));
+            TMEM_LD_WAIT((o + 0));
+            TMEM_LD_WAIT((o + 32));
           } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = 0u;
+            for (int c = 0; c < 64; ++c) o[c] = 0u;
           }
-          if (row) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 v;
-              v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]) * inv, __uint_as_float(o[8 * c + 1]) * inv);
-              v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * inv, __uint_as_float(o[8 * c + 3]) * inv);
-              v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * inv, __uint_as_float(o[8 * c + 5]) * inv);
-              v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * inv, __uint_as_float(o[8 * c + 7]) * inv);
-              dst[c0 / 8 + c] = v;
-            }
-          }
+          store_rows64(a, t, a.o, w, sm + L::kStore + warp * 4096, (warp & 3) * 32, c0, o, inv, lane);
         }
         if (row && a.lse) a.lse[at] = (m_run + __log2f(l)) * 0.69314718055994531f;
       }

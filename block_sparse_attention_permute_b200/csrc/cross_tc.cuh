@@ -87,24 +87,58 @@ __device__ __forceinline__ uint4 seen_bits(const CrossArgs& a, int b, int j0, in
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Writes zeros over the rows of a shared-memory tile (panels of 64 columns, 128
-// bytes a row) whose bit is not set, and makes them visible to MMAs and TMA
-// (whole warp).
+// Writes zeros over the rows 32 w0 .. 32 w0 + 63 of a shared-memory tile (panels
+// of 64 columns, 128 bytes a row) whose bit is not set, and makes them visible
+// to MMAs and TMA (whole warp): eight lanes a row, the row's bits being known to
+// all.
 template <int HD>
-__device__ __forceinline__ void zero_hidden_rows(uint8_t* tile, uint4 seen, int lane) {
-  const uint32_t m4[4] = {seen.x, seen.y, seen.z, seen.w};
+__device__ __forceinline__ void zero_hidden_rows(uint8_t* tile, uint4 seen, int w0, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (!((m4[i] >> lane) & 1u)) {
-      uint8_t* row = tile + (32 * i + lane) * 128;
+  for (int i = 0; i < 2; ++i) {
+    uint32_t hidden = ~(w0 + i == 0 ? seen.x : w0 + i == 1 ? seen.y : w0 + i == 2 ? seen.z : seen.w);
+    while (hidden) {       // four rows a time, a group of eight lanes each
+      uint32_t rest = hidden;
+      for (int g = lane >> 3; g > 0 && rest; --g) rest &= rest - 1;
+      if (rest) {
+        uint8_t* row = tile + (32 * (w0 + i) + __ffs(rest) - 1) * 128 + (lane & 7) * 16;
 #pragma unroll
-      for (int p = 0; p < HD / 64; ++p)
+        for (int p = 0; p < HD / 64; ++p)
+          *reinterpret_cast<uint4*>(row + p * 128 * 128) = make_uint4(0u, 0u, 0u, 0u);
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          reinterpret_cast<uint4*>(row + p * 128 * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
+      for (int g = 0; g < 4; ++g) hidden &= hidden - 1;
     }
+  }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Writes 64 columns (from column c0) of the warp's 32 rows of a query tile to a
+// per-token tensor, bf16(o * by): through `stage` (4 KB of the warp's own), so
+// that a store instruction covers whole 128-byte runs of four rows instead of
+// 16 bytes of 32.  `row0` is the tile row of lane 0.
+__device__ __forceinline__ void store_rows64(const CrossArgs& a, const CrossTiles& t, const View& v, const Work& w,
+                                             uint8_t* stage, int row0, int c0, const uint32_t (&o)[64], float by,
+                                             int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint4 u;
+    u.x = pack_bf16x2(__uint_as_float(o[8 * e + 0]) * by, __uint_as_float(o[8 * e + 1]) * by);
+    u.y = pack_bf16x2(__uint_as_float(o[8 * e + 2]) * by, __uint_as_float(o[8 * e + 3]) * by);
+    u.z = pack_bf16x2(__uint_as_float(o[8 * e + 4]) * by, __uint_as_float(o[8 * e + 5]) * by);
+    u.w = pack_bf16x2(__uint_as_float(o[8 * e + 6]) * by, __uint_as_float(o[8 * e + 7]) * by);
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = u;
+  }
+  __syncwarp();
+  __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(v.p) + w.b * v.b + c0 + (lane & 7) * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    const uint4 u = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+    const int rt = (int)fdiv((uint32_t)(row0 + r), t.div_pack), n = w.tok0 + rt, h = w.h0 + row0 + r - rt * t.pack;
+    if (w.real && rt < t.tokens && n < a.n_q) *reinterpret_cast<uint4*>(base + n * v.n + h * v.h) = u;
+  }
 }
 
 // Refuses to launch a build whose kernel does not get kRegsLaunch registers per

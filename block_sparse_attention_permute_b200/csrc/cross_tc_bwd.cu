@@ -31,7 +31,8 @@ struct DqLayout {
   static constexpr int kQ = 0, kDo = 2 * kTile, kK = 4 * kTile, kV = 6 * kTile;   // 2 Q, 2 dO, 2 K slots, 1 V
   static constexpr int kBars = 7 * kTile;
   static constexpr int kQFull = 0, kQEmpty = 2, kOFull = 4, kOEmpty = 6, kKFull = 8, kKEmpty = 10, kVFull = 12,
-                       kVEmpty = 13, kS = 14, kP = 16, kDp = 18, kDs = 20, kDq = 22, kFinal = 24, kNumBars = 25;
+                       kVEmpty = 13, kS = 14, kP = 16, kDp = 18, kDs = 20, kDq = 22, kFinal = 24, kKClean = 25,
+                       kVClean = 27, kNumBars = 28;
   static constexpr int kTmemSlot = kBars + kNumBars * 8, kAbort = kTmemSlot + 4;
   static constexpr int kAlloc = kAbort + 4 + 1024;
 };
@@ -109,10 +110,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kAbort);
   const long long lim = t.wait_limit > 0 ? t.wait_limit : kWaitLimitDefault;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool cleaning = a.key_mask != nullptr || a.kv_len != nullptr;
 
   if (threadIdx.x == 0) {
     for (int x = 0; x < L::kNumBars; ++x)
-      mbar_init(bar(x), x == L::kP || x == L::kP + 1 || x == L::kDs || x == L::kDs + 1 ? 128u : 1u);
+      mbar_init(bar(x), (x >= L::kP && x < L::kP + 2) || (x >= L::kDs && x < L::kDs + 2) ||
+                                (x >= L::kOEmpty && x < L::kOEmpty + 2)
+                            ? 128u
+                            : x >= L::kKClean ? 2u : 1u);
     *abort = 0;
     fence_mbar_init();
   }
@@ -181,21 +186,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait = [&](int b, int phase) {
         return __all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, abort, lim)) != 0;
       };
-      // Rows of K and V that are not attended become zeros: what they hold must
-      // not enter, not even times 0.
-      auto clean = [&](const Work& w, int s, int at) {
-        const int keys = cross_keys(a, w.b), j0 = (w.kt + s) * 128;
-        if (a.key_mask != nullptr || j0 + 128 > keys)
-          zero_hidden_rows<HD>(sm + at, seen_bits(a, w.b, j0, keys, lane), lane);
-      };
       int items = 0;
       // S of both streams for step g (x = 0 also takes the K tile)
       auto score = [&](const Cursor& c, int g, int x) -> bool {
         const int ks = g & 1;
         if (c.s == 0 && !wait(L::kQFull + x, items)) return false;
         if (x == 0) {
-          if (!wait(L::kKFull + ks, g >> 1)) return false;
-          clean(c.w, c.s, L::kK + ks * L::kTile);
+          if (!wait((cleaning ? L::kKClean : L::kKFull) + ks, g >> 1)) return false;
         }
         tc_fence_after();
         if (lane == 0) {
@@ -215,17 +212,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2 && ok; ++x) {
           if (c.s == 0) ok = wait(L::kOFull + x, items);
-          if (ok && x == 0) {
-            ok = wait(L::kVFull, g);
-            if (ok) clean(c.w, c.s, L::kV);
-          }
+          if (ok && x == 0) ok = wait(cleaning ? L::kVClean : L::kVFull, g);
           if (ok) ok = wait(L::kP + x, g);
           if (!ok) break;
           tc_fence_after();
           if (lane == 0) {
             mma_rows<HD>(tmem + 128u * x, sb + L::kDo + x * L::kTile, sb + L::kV);
             tc_commit(bar(L::kDp + x));
-            if (last) tc_commit(bar(L::kOEmpty + x));
             if (x == 1) tc_commit(bar(L::kVEmpty));
           }
           __syncwarp();
@@ -252,6 +245,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Every MMA issued is complete before TMEM is released, also after an abort.
       if (lane == 0) tc_commit(bar(L::kFinal));
       mbar_wait_drain(bar(L::kFinal), 0, lim);
+    } else if (warp >= 10 && cleaning) {
+      // ------------------------------------------------------------ cleaning
+      // What K and V hold at keys that are not attended must not enter, not even
+      // times 0: warps 10 and 11 write zeros over those rows, 64 rows each.
+      Cursor c;
+      int g = 0;
+      for (c.start(a, t, 0); c.valid(t); c.advance(a, t, 0), ++g) {
+        const int j0 = (c.w.kt + c.s) * 128, keys = cross_keys(a, c.w.b), ks = g & 1;
+        const bool hidden = a.key_mask != nullptr || j0 + 128 > keys;
+        uint4 m;
+        if (hidden) m = seen_bits(a, c.w.b, j0, keys, lane);
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kKFull + ks), (g >> 1) & 1, abort, lim))) break;
+        if (hidden) zero_hidden_rows<HD>(sm + L::kK + ks * L::kTile, m, 2 * (warp - 10), lane);
+        if (lane == 0) mbar_arrive(bar(L::kKClean + ks));
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kVFull), g & 1, abort, lim))) break;
+        if (hidden) zero_hidden_rows<HD>(sm + L::kV, m, 2 * (warp - 10), lane);
+        if (lane == 0) mbar_arrive(bar(L::kVClean));
+      }
     }
   } else {
     // ------------------------------------------------------------ rows
@@ -340,22 +351,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = w.tok0 + rt, h = w.h0 + rg;
       const bool row = w.real && n < a.n_q;
       const long long at = ((long long)w.b * a.heads + h) * a.n_q + n;
+      if (a.splits > 1 || w.n == 0) {
 #pragma unroll
-      for (int c0 = 0; c0 < HD; c0 += 32) {
-        uint32_t o[32];
-        if (w.n > 0) {
-          TMEM_LD32(tQ + c0, o);
-          TMEM_LD_WAIT(o);
-        } else {
+        for (int c0 = 0; c0 < HD; c0 += 32) {
+          uint32_t o[32];
+          if (w.n > 0) {
+            TMEM_LD32(tQ + c0, o);
+            TMEM_LD_WAIT(o);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0u;
-        }
-        if (row) {
-          if (a.splits > 1)
-            store32(a.part_o + (w.split * rows + at) * HD + c0, o, a.scale);
-          else
+            for (int c = 0; c < 32; ++c) o[c] = 0u;
+          }
+          if (row && a.splits > 1) store32(a.part_o + (w.split * rows + at) * HD + c0, o, a.scale);
+          if (row && a.splits == 1)
             store32(reinterpret_cast<__nv_bfloat16*>(a.dq.p) + w.b * a.dq.b + n * a.dq.n + h * a.dq.h + c0, o, a.scale);
         }
+      } else {
+        // every MMA that reads the stream's dO is done: its place serves the
+        // stores, and only then takes the next item's
+#pragma unroll
+        for (int c0 = 0; c0 < HD; c0 += 64) {
+          uint32_t o[64];
+          TMEM_LD32(tQ + c0, (o + 0));
+          TMEM_LD32(tQ + c0 + 32, (o + 32));
+          TMEM_LD_WAIT((o + 0));
+          TMEM_LD_WAIT((o + 32));
+          store_rows64(a, t, a.dq, w, sm + L::kDo + x * L::kTile + (warp & 3) * 4096, (warp & 3) * 32, c0, o, a.scale,
+                       lane);
+        }
+      }
+      if (w.n > 0) {
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::kOEmpty + x));
       }
       tc_fence_before();
     }
