@@ -133,8 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int p = pos[y] > L::kStages ? pos[y] - L::kStages : 0; p < pos[y]; ++p)
           mbar_wait_drain(bar(L::kFull + y * L::kStages + p % L::kStages), (p / L::kStages) & 1, lim);
     } else if (warp == 9) {
-      // ------------------------------------------------------------ MMAs (the whole warp waits, lane 0 issues)
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0), idesc_o = idesc_bf16_f32(128, HD, 0, 1);
+      // ------------------------------------------------------------ MMAs (the whole warp waits, one lane issues)
       int pos[2] = {0, 0}, kept[2] = {0, 0}, nq[2] = {0, 0}, np[2] = {0, 0};
       auto wait = [&](uint32_t b, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(b, parity, abort, lim)) != 0;
@@ -160,22 +159,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t tS = tmem + 128u * x, tO = tmem + 256u + 128u * x;
-        if (lane == 0) {
+        if (elect_one()) {
           if (kind == 0) {
-            const uint32_t sQ = sb + L::kQ + x * L::kTile;
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * L::kPanel + (kk & 3) * 32;
-              mma_bf16_ss(tS, smem_desc_sw128(sQ + off, 16, 1024), smem_desc_sw128(src + off, 16, 1024), idesc_s,
-                          kk > 0 ? 1u : 0u);
-            }
+            mma_rows<HD>(tS, sb + L::kQ + x * L::kTile, src);
             tc_commit(bar(L::kS + x));
             if (c.s == w.n - 1) tc_commit(bar(L::kQEmpty + x));
           } else {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ts(tO, tS + 8u * kk, smem_desc_sw128(src + kk * 2048, L::kPanel, 1024), idesc_o,
-                          (c.s > 0 || kk > 0) ? 1u : 0u);
+            mma_cols<HD>(tO, tS, 32u, src, c.s > 0);
             if (c.s == w.n - 1) tc_commit(bar(L::kO + x));
           }
           if (!t.shared || x == 1) tc_commit(bar(L::kEmpty + slot));
@@ -184,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       });
       // Every MMA issued is complete before TMEM is released, also after an abort.
-      if (lane == 0) tc_commit(bar(L::kFinal));
+      if (elect_one()) tc_commit(bar(L::kFinal));
       mbar_wait_drain(bar(L::kFinal), 0, lim);
     } else if (warp >= 10 && cleaning) {
       // ------------------------------------------------------------ cleaning of V

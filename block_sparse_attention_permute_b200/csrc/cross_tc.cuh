@@ -74,6 +74,62 @@ struct Cursor {
   }
 };
 
+// True in one lane of the warp, always the same one (the one that issues MMAs
+// and their commits); the branch on it leaves the warp's values uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Products of 128-row tiles in shared memory (128-byte swizzle, panels of 64
+// columns).  Only the low word of an operand's descriptor (address and leading
+// offset) changes from one MMA to the next, by a constant: the issuing thread
+// adds, it does not build descriptors (building them took longer than the MMA:
+// 125 cycles per 128 x 128 x 16 product instead of 64 to 80).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lead_bytes) {
+  return (saddr >> 4) | ((lead_bytes >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
+      : "memory");
+}
+// D = A B^T: both operands contracted over the head dimension.
+template <int HD>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb) {
+  const uint32_t a = desc_low(sa, 16), b = desc_low(sb, 16);
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2;
+    mma_ss(d, a + off, b + off, idesc_bf16_f32(128, 128, 0, 0), kk > 0 ? 1u : 0u);
+  }
+}
+// D (+)= A B: A bf16 in TMEM (128 values of a row as pairs; the second half
+// starts `half` columns after the first), B's 128 rows contracted.
+template <int HD>
+__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t ta, uint32_t half, uint32_t sb, bool accumulate) {
+  const uint32_t b = desc_low(sb, 128 * 128);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(d, ta + (kk >> 2) * half + 8u * (kk & 3), b + kk * (2048 / 16), idesc_bf16_f32(128, HD, 0, 1),
+           (accumulate || kk > 0) ? 1u : 0u);
+}
+
 // Bit c of word w: key j0 + 32 w + c is attended (whole warp).
 __device__ __forceinline__ uint4 seen_bits(const CrossArgs& a, int b, int j0, int keys, int lane) {
   uint32_t w[4];

@@ -51,27 +51,6 @@ struct DkvLayout {
   static constexpr int kAlloc = kAbort + 4 + 1024;
 };
 
-// D (+)= A B^T: both operands tiles of 128 rows, the head dimension contracted.
-template <int HD>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb) {
-#pragma unroll
-  for (int kk = 0; kk < HD / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-    mma_bf16_ss(d, smem_desc_sw128(sa + off, 16, 1024), smem_desc_sw128(sb + off, 16, 1024),
-                idesc_bf16_f32(128, 128, 0, 0), kk > 0 ? 1u : 0u);
-  }
-}
-
-// D (+)= A B: A bf16 in TMEM (128 columns of values as pairs; its second half
-// starts `half` columns after the first), B a tile of 128 rows, contracted.
-template <int HD>
-__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t ta, uint32_t half, uint32_t sb, bool accumulate) {
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_bf16_ts(d, ta + (kk >> 2) * half + 8u * (kk & 3), smem_desc_sw128(sb + kk * 2048, 128 * 128, 1024),
-                idesc_bf16_f32(128, HD, 0, 1), (accumulate || kk > 0) ? 1u : 0u);
-}
-
 template <int HD>
 __device__ __forceinline__ void load_tile4(uint32_t dst, const CUtensorMap* map, int h, int n, int b, uint32_t bar) {
 #pragma unroll
@@ -182,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (nv > 0) mbar_wait_drain(bar(L::kVFull), (nv - 1) & 1, lim);
     } else if (warp == 9) {
-      // ------------------------------------------------------------ MMAs (the whole warp waits, lane 0 issues)
+      // ------------------------------------------------------------ MMAs (the whole warp waits, one lane issues)
       auto wait = [&](int b, int phase) {
         return __all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, abort, lim)) != 0;
       };
@@ -195,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait((cleaning ? L::kKClean : L::kKFull) + ks, g >> 1)) return false;
         }
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           mma_rows<HD>(tmem + 128u * x, sb + L::kQ + x * L::kTile, sb + L::kK + ks * L::kTile);
           tc_commit(bar(L::kS + x));
           if (c.s == c.w.n - 1) tc_commit(bar(L::kQEmpty + x));
@@ -216,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) ok = wait(L::kP + x, g);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             mma_rows<HD>(tmem + 128u * x, sb + L::kDo + x * L::kTile, sb + L::kV);
             tc_commit(bar(L::kDp + x));
             if (x == 1) tc_commit(bar(L::kVEmpty));
@@ -232,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(L::kDs + x, g);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             mma_cols<HD>(tmem + 256u + 128u * x, tmem + 128u * x, 32u, sb + L::kK + (g & 1) * L::kTile, c.s > 0);
             if (last) tc_commit(bar(L::kDq + x));
             if (x == 1) tc_commit(bar(L::kKEmpty + (g & 1)));
@@ -243,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         c = next;
       }
       // Every MMA issued is complete before TMEM is released, also after an abort.
-      if (lane == 0) tc_commit(bar(L::kFinal));
+      if (elect_one()) tc_commit(bar(L::kFinal));
       mbar_wait_drain(bar(L::kFinal), 0, lim);
     } else if (warp >= 10 && cleaning) {
       // ------------------------------------------------------------ cleaning
@@ -462,42 +441,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(bar(L::kQFull + i % L::kStages), (i / L::kStages) & 1, lim);
       for (int i = no > L::kStages ? no - L::kStages : 0; i < no; ++i)
         mbar_wait_drain(bar(L::kOFull + i % L::kStages), (i / L::kStages) & 1, lim);
-    } else if (warp == 9 && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ MMAs
+    } else if (warp == 9 && n > 0) {
+      // ------------------------------------------------------------ MMAs (the whole warp waits, one lane issues)
       auto wait = [&](int x, int phase) {
-        const bool ok = mbar_wait(bar(x), phase & 1, abort, lim);
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(x), phase & 1, abort, lim)) != 0;
         tc_fence_after();
         return ok;
       };
       auto scores = [&](int i) {      // S^T of query tile i
         const int st = i % L::kStages;
         if (!wait(L::kQFull + st, i / L::kStages)) return false;
-        mma_rows<HD>(tS, sb + L::kK, sb + L::kQ + st * L::kTile);
-        tc_commit(bar(L::kS));
+        if (elect_one()) {
+          mma_rows<HD>(tS, sb + L::kK, sb + L::kQ + st * L::kTile);
+          tc_commit(bar(L::kS));
+        }
+        __syncwarp();
         return true;
       };
       auto slopes = [&](int i) {      // dP^T of query tile i
         const int st = i % L::kStages;
         if (!wait(L::kOFull + st, i / L::kStages)) return false;
-        mma_rows<HD>(tD, sb + L::kV, sb + L::kDo + st * L::kTile);
-        tc_commit(bar(L::kDp));
+        if (elect_one()) {
+          mma_rows<HD>(tD, sb + L::kV, sb + L::kDo + st * L::kTile);
+          tc_commit(bar(L::kDp));
+        }
+        __syncwarp();
         return true;
       };
       bool ok = wait(L::kKv, 0) && scores(0) && slopes(0);
       for (int i = 0; ok && i < n; ++i) {
         const int st = i % L::kStages;
         if (!wait(L::kP, i)) break;
-        mma_cols<HD>(tV, tS, 64u, sb + L::kDo + st * L::kTile, i > 0);
-        tc_commit(bar(L::kOEmpty + st));
+        if (elect_one()) {
+          mma_cols<HD>(tV, tS, 64u, sb + L::kDo + st * L::kTile, i > 0);
+          tc_commit(bar(L::kOEmpty + st));
+        }
+        __syncwarp();
         if (i + 1 < n && !scores(i + 1)) break;
         if (!wait(L::kDs, i)) break;
-        mma_cols<HD>(tK, tD, 64u, sb + L::kQ + st * L::kTile, i > 0);
-        tc_commit(bar(L::kQEmpty + st));
+        if (elect_one()) {
+          mma_cols<HD>(tK, tD, 64u, sb + L::kQ + st * L::kTile, i > 0);
+          tc_commit(bar(L::kQEmpty + st));
+        }
+        __syncwarp();
         if (i + 1 < n && !slopes(i + 1)) break;
       }
       // The row threads read dK and dV after this; every MMA issued is complete
       // before TMEM is released, also after an abort.
-      tc_commit(bar(L::kFinal));
+      if (elect_one()) tc_commit(bar(L::kFinal));
       mbar_wait_drain(bar(L::kFinal), 0, lim);
     }
   } else {
