@@ -49,6 +49,7 @@ __device__ __forceinline__ int cross_keys(const CrossArgs& a, int b) {
 struct CrossTiles {
   int tiles;        // query tiles of one (batch element, K/V head)
   int tokens, pack; // tokens * pack <= 128
+  int bulk_out;     // a warp's 32 rows are whole tokens: the output goes by TMA (map `out`, 32 rows a box)
   int shared;       // streams take two query tiles over the same keys (else one over two key runs)
   int items;        // (batch element, K/V head, split, item of it), the last fastest
   int ctas;         // CTAs at a time (one per SM)
@@ -59,7 +60,7 @@ struct CrossTiles {
 };
 // Tensor maps (d, head, token, batch) of the views.
 struct CrossMaps {
-  CUtensorMap q, k, v, d_o;
+  CUtensorMap q, k, v, d_o, out;   // out: o of the forward, dq of the backward
 };
 
 // cross_tc.cu (bf16)

@@ -62,6 +62,7 @@ void plan_tiles(const bsa_cross_s* c, bool whole, bsa::CrossTiles* t) {
     if (tiles == 0 || n < tiles) tiles = n, t->pack = p, t->tokens = tokens;
   }
   t->tiles = (int)tiles;
+  t->bulk_out = 32 % t->pack == 0;
   t->ctas = kSms;
   t->div_hkv = make_fastdiv((uint32_t)c->heads_kv);
   t->div_tok = make_fastdiv((uint32_t)((c->n_q + t->tokens - 1) / t->tokens));
@@ -188,6 +189,10 @@ bsa_status make_maps(const bsa_cross_s* p, const bsa::CrossArgs& a, bool backwar
     return s;
   if (backward && (s = make_map(&m->d_o, a.d_o, p->B, p->n_q, p->heads, p->D, t->pack, t->tokens, &t->step_ob,
                                 &t->step_oh)) != BSA_OK)
+    return s;
+  int step_b, step_h;      // (an output repeats along no axis)
+  if (t->bulk_out && (s = make_map(&m->out, backward ? a.dq : a.o, p->B, p->n_q, p->heads, p->D, t->pack, 32 / t->pack,
+                                   &step_b, &step_h)) != BSA_OK)
     return s;
   t->wait_limit = p->wait_limit;
   t->hold_load = p->hold_load;

@@ -322,12 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 64; ++c) o[c] = 0u;
           }
-          store_rows64(a, t, a.o, w, sm + L::kStore + warp * 4096, (warp & 3) * 32, c0, o, inv, lane);
+          // the warp's staging holds 64 columns: the store before has to have read it
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          store_rows64(a, t, &maps.out, a.o, w, sm + L::kStore + warp * 4096, (warp & 3) * 32, c0, o, inv, lane);
         }
         if (row && a.lse) a.lse[at] = (m_run + __log2f(l)) * 0.69314718055994531f;
       }
       tc_fence_before();
     }
+    if (lane == 0) bulk_wait();
   }
 
   tc_fence_before();

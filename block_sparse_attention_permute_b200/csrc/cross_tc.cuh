@@ -169,14 +169,14 @@ __device__ __forceinline__ void zero_hidden_rows(uint8_t* tile, uint4 seen, int 
   __syncwarp();
 }
 
-// Writes 64 columns (from column c0) of the warp's 32 rows of a query tile to a
-// per-token tensor, bf16(o * by): through `stage` (4 KB of the warp's own), so
-// that a store instruction covers whole 128-byte runs of four rows instead of
-// 16 bytes of 32.  `row0` is the tile row of lane 0.
-__device__ __forceinline__ void store_rows64(const CrossArgs& a, const CrossTiles& t, const View& v, const Work& w,
-                                             uint8_t* stage, int row0, int c0, const uint32_t (&o)[64], float by,
-                                             int lane) {
-  __syncwarp();
+// Writes 64 columns (from column c0) of the warp's 32 rows of a query tile (tile
+// rows row0 ..) to a per-token tensor, bf16(o * by), through `stage` (4 KB of the
+// warp's own, 1024-byte aligned, no longer read): as one TMA store of lane 0's
+// next bulk group, or, where a warp's rows are not whole tokens, with stores of
+// 128 bytes of four rows each instead of 16 bytes of 32.
+__device__ __forceinline__ void store_rows64(const CrossArgs& a, const CrossTiles& t, const CUtensorMap* map,
+                                             const View& v, const Work& w, uint8_t* stage, int row0, int c0,
+                                             const uint32_t* o, float by, int lane) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint4 u;
@@ -185,6 +185,15 @@ __device__ __forceinline__ void store_rows64(const CrossArgs& a, const CrossTile
     u.z = pack_bf16x2(__uint_as_float(o[8 * e + 4]) * by, __uint_as_float(o[8 * e + 5]) * by);
     u.w = pack_bf16x2(__uint_as_float(o[8 * e + 6]) * by, __uint_as_float(o[8 * e + 7]) * by);
     *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = u;
+  }
+  if (t.bulk_out) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && w.real) {
+      tma_store_4d(map, smem_addr(stage), c0, w.h0, w.tok0 + (int)fdiv((uint32_t)row0, t.div_pack), w.b);
+      bulk_commit();
+    }
+    return;
   }
   __syncwarp();
   __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(v.p) + w.b * v.b + c0 + (lane & 7) * 8;
@@ -195,6 +204,7 @@ __device__ __forceinline__ void store_rows64(const CrossArgs& a, const CrossTile
     const int rt = (int)fdiv((uint32_t)(row0 + r), t.div_pack), n = w.tok0 + rt, h = w.h0 + row0 + r - rt * t.pack;
     if (w.real && rt < t.tokens && n < a.n_q) *reinterpret_cast<uint4*>(base + n * v.n + h * v.h) = u;
   }
+  __syncwarp();
 }
 
 // Refuses to launch a build whose kernel does not get kRegsLaunch registers per

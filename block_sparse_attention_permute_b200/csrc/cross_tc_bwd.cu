@@ -355,9 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           TMEM_LD32(tQ + c0 + 32, (o + 32));
           TMEM_LD_WAIT((o + 0));
           TMEM_LD_WAIT((o + 32));
-          store_rows64(a, t, a.dq, w, sm + L::kDo + x * L::kTile + (warp & 3) * 4096, (warp & 3) * 32, c0, o, a.scale,
-                       lane);
+          store_rows64(a, t, &maps.out, a.dq, w, sm + L::kDo + x * L::kTile + (warp & 3) * (L::kTile / 4) + c0 * 64,
+                       (warp & 3) * 32, c0, o, a.scale, lane);
         }
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
       }
       if (w.n > 0) {
         fence_proxy_async_smem();
@@ -365,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
+    if (lane == 0) bulk_wait();
   }
 
   tc_fence_before();
