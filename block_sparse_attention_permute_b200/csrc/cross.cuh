@@ -25,7 +25,7 @@ struct CrossArgs {
   float* part_kv;
   int B, n_q, n_kv, heads, heads_kv, group;
   int splits;                // of the kernel at hand
-  int split_len;             // key tiles (forward) or row tiles (dK, dV) per split
+  int split_len;             // key tiles or steps (forward, dQ) or row tiles (dK, dV) per split
   float scale, scale_log2;   // softmax scale, and times log2(e)
   int32_t* status;
 };
@@ -51,6 +51,7 @@ struct CrossTiles {
   int tokens, pack; // tokens * pack <= 128
   int bulk_out;     // a warp's 32 rows are whole tokens: the output goes by TMA (map `out`, 32 rows a box)
   int shared;       // streams take two query tiles over the same keys (else one over two key runs)
+  int step;         // keys of a step (CrossArgs::split_len counts these)
   int items;        // (batch element, K/V head, split, item of it), the last fastest
   int ctas;         // CTAs at a time (one per SM)
   FastDiv div_items, div_splits, div_hkv, div_tok, div_pack;

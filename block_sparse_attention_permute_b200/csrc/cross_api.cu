@@ -79,20 +79,24 @@ void plan_items(const bsa_cross_s* c, int per, int splits, bsa::CrossTiles* t) {
 // The schedules of the tensor-core kernels.
 void plan_tc(bsa_cross_s* c) {
   const long long bh = (long long)c->B * c->heads_kv;
-  const int key_tiles = (c->n_kv + 127) / 128;
   plan_tiles(c, false, &c->fwd);
   // Two tiles per item over the same keys, or one tile over two runs of keys
-  // (always merged): whichever the estimate says ends first, a round of both
-  // streams being the unit and partials and merge costing about three rounds.
+  // (always merged): whichever the estimate says ends first, a step of both
+  // streams being the unit, an item's start and end about one and a half of them,
+  // partials and merge about three.
   const int tiles = c->fwd.tiles;
+  c->fwd.step = 128;
+  const int steps = (c->n_kv + 127) / 128;
   double pair, dual;
-  const int len = split_units(bh * ((tiles + 1) / 2), key_tiles, kSms, 1.0, 3.0, &pair);
-  const int half = split_units(bh * tiles, (key_tiles + 1) / 2, kSms, 1.0, 0.0, &dual);
-  c->fwd.shared = key_tiles == 1 || pair <= dual + 3.0;
+  const int len = split_units(bh * ((tiles + 1) / 2), steps, kSms, 1.5, 3.0, &pair);
+  const int half = split_units(bh * tiles, (steps + 1) / 2, kSms, 1.5, 0.0, &dual);
+  c->fwd.shared = steps == 1 || pair <= dual + 3.0;
   c->fwd_len = c->fwd.shared ? len : 2 * half;
-  const int splits = (key_tiles + c->fwd_len - 1) / c->fwd_len;
+  const int splits = (steps + c->fwd_len - 1) / c->fwd_len;
   c->fwd_splits = c->fwd.shared ? splits : 2 * splits;
   plan_items(c, c->fwd.shared ? (tiles + 1) / 2 : tiles, splits, &c->fwd);
+  const int key_tiles = (c->n_kv + 127) / 128;
+  c->bwd.step = 128;
   plan_tiles(c, true, &c->bwd);
   c->bwd.shared = 1;
   const int pairs = (c->bwd.tiles + 1) / 2;
@@ -184,8 +188,8 @@ bsa_status make_maps(const bsa_cross_s* p, const bsa::CrossArgs& a, bool backwar
   std::memset(m, 0, sizeof(*m));
   bsa_status s;
   if ((s = make_map(&m->q, a.q, p->B, p->n_q, p->heads, p->D, t->pack, t->tokens, &t->step_qb, &t->step_qh)) != BSA_OK ||
-      (s = make_map(&m->k, a.k, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t->step_kb, &t->step_kh)) != BSA_OK ||
-      (s = make_map(&m->v, a.v, p->B, p->n_kv, p->heads_kv, p->D, 1, 128, &t->step_vb, &t->step_vh)) != BSA_OK)
+      (s = make_map(&m->k, a.k, p->B, p->n_kv, p->heads_kv, p->D, 1, t->step, &t->step_kb, &t->step_kh)) != BSA_OK ||
+      (s = make_map(&m->v, a.v, p->B, p->n_kv, p->heads_kv, p->D, 1, t->step, &t->step_vb, &t->step_vh)) != BSA_OK)
     return s;
   if (backward && (s = make_map(&m->d_o, a.d_o, p->B, p->n_q, p->heads, p->D, t->pack, t->tokens, &t->step_ob,
                                 &t->step_oh)) != BSA_OK)

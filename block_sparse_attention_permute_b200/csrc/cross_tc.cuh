@@ -16,60 +16,71 @@ struct RegSplit {
   static __device__ __forceinline__ void small() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SMALL)); }
 };
 
-// What an item gives to one stream.
+// An item of the schedule: a K/V head of a batch element, a run of key steps, a
+// pair of query tiles (or one).
 struct Work {
-  int b, hk, h0, tok0;   // batch element, K/V head, first head and token of the query tile
-  int kt, n;             // key tiles kt .. kt + n - 1
-  int split;             // index of its partial
-  int row_tile;          // its place among all query tiles
-  bool real;             // false: the padding tile of an odd pair
+  int b, hk, bh;      // batch element, K/V head, and both as one index
+  int keys;           // keys of the batch element
+  int i, split;       // place among the head's items, key split
+  int kt, n;          // first key step, steps (of stream 0 where the streams halve them)
+  int all;            // steps of both streams together where they halve them, else n
+  bool halved;
+  // Steps of stream x and the first of them.
+  __device__ __forceinline__ int steps(int x) const { return halved && x ? all - n : n; }
+  __device__ __forceinline__ int first(int x) const { return halved && x ? kt + n : kt; }
 };
 
-__device__ __forceinline__ Work decode(const CrossArgs& a, const CrossTiles& t, int it, int x) {
+__device__ __forceinline__ Work decode(const CrossArgs& a, const CrossTiles& t, int it) {
   Work w;
-  const int rest = (int)fdiv((uint32_t)it, t.div_items), i = it - rest * (int)t.div_items.d;
-  const int bh = (int)fdiv((uint32_t)rest, t.div_splits);
-  w.split = rest - bh * (int)t.div_splits.d;
-  w.b = (int)fdiv((uint32_t)bh, t.div_hkv);
-  w.hk = bh - w.b * a.heads_kv;
-  const int tile = t.shared ? 2 * i + x : i;
-  const int sg = (int)fdiv((uint32_t)tile, t.div_tok), tt = tile - sg * (int)t.div_tok.d;
-  w.real = tile < t.tiles;
-  w.row_tile = bh * t.tiles + tile;
-  w.h0 = w.hk * a.group + sg * t.pack;
-  w.tok0 = tt * t.tokens;
-  const int tiles = (cross_keys(a, w.b) + 127) >> 7;
+  const int rest = (int)fdiv((uint32_t)it, t.div_items);
+  w.i = it - rest * (int)t.div_items.d;
+  w.bh = (int)fdiv((uint32_t)rest, t.div_splits);
+  w.split = rest - w.bh * (int)t.div_splits.d;
+  w.b = (int)fdiv((uint32_t)w.bh, t.div_hkv);
+  w.hk = w.bh - w.b * a.heads_kv;
+  w.keys = cross_keys(a, w.b);
   w.kt = w.split * a.split_len;
-  w.n = max(0, min(a.split_len, tiles - w.kt));
-  if (!t.shared) {
-    const int first = (w.n + 1) >> 1;
-    w.split = 2 * w.split + x;
-    if (x) w.kt += first;
-    w.n = x ? w.n - first : first;
-  }
+  w.all = max(0, min(a.split_len, (w.keys + t.step - 1) / t.step - w.kt));
+  w.halved = !t.shared;
+  w.n = w.halved ? (w.all + 1) >> 1 : w.all;
   return w;
 }
 
-// Walks the steps of one stream over the CTA's items.
+// The query tile that an item gives to stream x.
+struct RowTile {
+  int h0, tok0;   // first head and token
+  int at;         // place among all query tiles
+  bool real;      // false: the padding tile of an odd pair
+};
+__device__ __forceinline__ RowTile row_tile(const CrossArgs& a, const CrossTiles& t, const Work& w, int x) {
+  const int tile = t.shared ? 2 * w.i + x : w.i;
+  const int sg = (int)fdiv((uint32_t)tile, t.div_tok);
+  return {w.hk * a.group + sg * t.pack, (tile - sg * (int)t.div_tok.d) * t.tokens, w.bh * t.tiles + tile,
+          tile < t.tiles};
+}
+
+// Walks the steps of the CTA's items, both streams in step.
 struct Cursor {
   int it, s;
   Work w;
   __device__ __forceinline__ bool valid(const CrossTiles& t) const { return it < t.items; }
-  __device__ __forceinline__ void find(const CrossArgs& a, const CrossTiles& t, int x) {
+  __device__ __forceinline__ bool active(int x) const { return s < w.steps(x); }
+  __device__ __forceinline__ int key_step(int x) const { return w.first(x) + s; }
+  __device__ __forceinline__ void find(const CrossArgs& a, const CrossTiles& t) {
     for (; it < t.items; it += gridDim.x) {
-      w = decode(a, t, it, x);
+      w = decode(a, t, it);
       if (w.n > 0) break;
     }
     s = 0;
   }
-  __device__ __forceinline__ void start(const CrossArgs& a, const CrossTiles& t, int x) {
+  __device__ __forceinline__ void start(const CrossArgs& a, const CrossTiles& t) {
     it = blockIdx.x;
-    find(a, t, x);
+    find(a, t);
   }
-  __device__ __forceinline__ void advance(const CrossArgs& a, const CrossTiles& t, int x) {
+  __device__ __forceinline__ void advance(const CrossArgs& a, const CrossTiles& t) {
     if (++s == w.n) {
       it += gridDim.x;
-      find(a, t, x);
+      find(a, t);
     }
   }
 };
@@ -109,74 +120,59 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, 
       "r"(a_tmem), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
       : "memory");
 }
-// D = A B^T: both operands contracted over the head dimension.
-template <int HD>
+// D = A B^T: 128 rows of A, N rows of B, contracted over the head dimension.
+template <int HD, int N = 128>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb) {
   const uint32_t a = desc_low(sa, 16), b = desc_low(sb, 16);
 #pragma unroll
   for (int kk = 0; kk < HD / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2;
-    mma_ss(d, a + off, b + off, idesc_bf16_f32(128, 128, 0, 0), kk > 0 ? 1u : 0u);
+    const uint32_t p = kk >> 2, c = (kk & 3) * 2;
+    mma_ss(d, a + p * (128 * 128 / 16) + c, b + p * (N * 128 / 16) + c, idesc_bf16_f32(128, N, 0, 0), kk > 0 ? 1u : 0u);
   }
 }
-// D (+)= A B: A bf16 in TMEM (128 values of a row as pairs; the second half
-// starts `half` columns after the first), B's 128 rows contracted.
-template <int HD>
+// D (+)= A B: A bf16 in TMEM (N values of a row as pairs; of 128, the second half
+// starts `half` columns after the first), B's N rows contracted.
+template <int HD, int N = 128>
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t ta, uint32_t half, uint32_t sb, bool accumulate) {
-  const uint32_t b = desc_low(sb, 128 * 128);
+  const uint32_t b = desc_low(sb, N * 128);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
+  for (int kk = 0; kk < N / 16; ++kk)
     mma_ts(d, ta + (kk >> 2) * half + 8u * (kk & 3), b + kk * (2048 / 16), idesc_bf16_f32(128, HD, 0, 1),
            (accumulate || kk > 0) ? 1u : 0u);
 }
 
-// Bit c of word w: key j0 + 32 w + c is attended (whole warp).
-__device__ __forceinline__ uint4 seen_bits(const CrossArgs& a, int b, int j0, int keys, int lane) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = j0 + 32 * i + lane;
-    bool s = j < keys;
-    if (s && a.key_mask) s = __ldg(a.key_mask + (long long)b * a.n_kv + j) != 0;
-    w[i] = __ballot_sync(0xffffffffu, s);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// Bit c: key j0 + c is attended (whole warp).
+__device__ __forceinline__ uint32_t seen_word(const CrossArgs& a, int b, int j0, int keys, int lane) {
+  const int j = j0 + lane;
+  bool s = j < keys;
+  if (s && a.key_mask) s = __ldg(a.key_mask + (long long)b * a.n_kv + j) != 0;
+  return __ballot_sync(0xffffffffu, s);
 }
 
-// Writes zeros over the rows 32 w0 .. 32 w0 + 63 of a shared-memory tile (panels
-// of 64 columns, 128 bytes a row) whose bit is not set, and makes them visible
-// to MMAs and TMA (whole warp): eight lanes a row, the row's bits being known to
-// all.
+// Writes zeros over the rows of a shared-memory tile (128 bytes a row in each of
+// its panels of 64 columns) whose bit in `hidden` is set, and makes them visible
+// to MMAs and TMA (whole warp): four rows a time, a group of eight lanes each.
 template <int HD>
-__device__ __forceinline__ void zero_hidden_rows(uint8_t* tile, uint4 seen, int w0, int lane) {
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int panel, uint32_t hidden, int lane) {
+  while (hidden) {
+    uint32_t rest = hidden;
+    for (int g = lane >> 3; g > 0 && rest; --g) rest &= rest - 1;
+    if (rest) {
+      uint8_t* row = tile + (__ffs(rest) - 1) * 128 + (lane & 7) * 16;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t hidden = ~(w0 + i == 0 ? seen.x : w0 + i == 1 ? seen.y : w0 + i == 2 ? seen.z : seen.w);
-    while (hidden) {       // four rows a time, a group of eight lanes each
-      uint32_t rest = hidden;
-      for (int g = lane >> 3; g > 0 && rest; --g) rest &= rest - 1;
-      if (rest) {
-        uint8_t* row = tile + (32 * (w0 + i) + __ffs(rest) - 1) * 128 + (lane & 7) * 16;
-#pragma unroll
-        for (int p = 0; p < HD / 64; ++p)
-          *reinterpret_cast<uint4*>(row + p * 128 * 128) = make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) hidden &= hidden - 1;
+      for (int p = 0; p < HD / 64; ++p) *reinterpret_cast<uint4*>(row + p * panel) = make_uint4(0u, 0u, 0u, 0u);
     }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) hidden &= hidden - 1;
   }
   fence_proxy_async_smem();
   __syncwarp();
 }
 
-// Writes 64 columns (from column c0) of the warp's 32 rows of a query tile (tile
-// rows row0 ..) to a per-token tensor, bf16(o * by), through `stage` (4 KB of the
-// warp's own, 1024-byte aligned, no longer read): as one TMA store of lane 0's
-// next bulk group, or, where a warp's rows are not whole tokens, with stores of
-// 128 bytes of four rows each instead of 16 bytes of 32.
-__device__ __forceinline__ void store_rows64(const CrossArgs& a, const CrossTiles& t, const CUtensorMap* map,
-                                             const View& v, const Work& w, uint8_t* stage, int row0, int c0,
-                                             const uint32_t* o, float by, int lane) {
+// Output rows go from registers to a per-token tensor through shared memory: 32
+// rows of the warp's own, 64 columns (4 KB, 1024-byte aligned) at a time, as
+// bf16(o * by) in the 128-byte swizzle ...
+__device__ __forceinline__ void stage_rows64(uint8_t* stage, const uint32_t* o, float by, int lane) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint4 u;
@@ -186,24 +182,37 @@ __device__ __forceinline__ void store_rows64(const CrossArgs& a, const CrossTile
     u.w = pack_bf16x2(__uint_as_float(o[8 * e + 6]) * by, __uint_as_float(o[8 * e + 7]) * by);
     *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = u;
   }
+}
+// ... and from there (tile rows row0 .. row0 + 31, whole warp) by TMA, in lane
+// 0's next bulk group, or, where a warp's rows are not whole tokens, with stores
+// of 128 bytes of four rows each (after which the stage is no longer read).
+template <int HD>
+__device__ __forceinline__ void store_rows(const CrossArgs& a, const CrossTiles& t, const CUtensorMap* map,
+                                           const View& v, int b, const RowTile& q, uint8_t* stage, int row0, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
   if (t.bulk_out) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0 && w.real) {
-      tma_store_4d(map, smem_addr(stage), c0, w.h0, w.tok0 + (int)fdiv((uint32_t)row0, t.div_pack), w.b);
+    if (lane == 0 && q.real) {
+      const int tok = q.tok0 + (int)fdiv((uint32_t)row0, t.div_pack);
+#pragma unroll
+      for (int c0 = 0; c0 < HD; c0 += 64) tma_store_4d(map, smem_addr(stage + c0 * 64), c0, q.h0, tok, b);
       bulk_commit();
     }
     return;
   }
-  __syncwarp();
-  __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(v.p) + w.b * v.b + c0 + (lane & 7) * 8;
-#pragma unroll
+  __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(v.p) + b * v.b + (lane & 7) * 8;
+#pragma unroll 1
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (lane >> 3);
-    const uint4 u = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-    const int rt = (int)fdiv((uint32_t)(row0 + r), t.div_pack), n = w.tok0 + rt, h = w.h0 + row0 + r - rt * t.pack;
-    if (w.real && rt < t.tokens && n < a.n_q) *reinterpret_cast<uint4*>(base + n * v.n + h * v.h) = u;
+    const int rt = (int)fdiv((uint32_t)(row0 + r), t.div_pack), n = q.tok0 + rt, h = q.h0 + row0 + r - rt * t.pack;
+    if (q.real && rt < t.tokens && n < a.n_q) {
+#pragma unroll
+      for (int c0 = 0; c0 < HD; c0 += 64)
+        *reinterpret_cast<uint4*>(base + c0 + n * v.n + h * v.h) =
+            *reinterpret_cast<const uint4*>(stage + c0 * 64 + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+    }
   }
+  fence_proxy_async_smem();
   __syncwarp();
 }
 

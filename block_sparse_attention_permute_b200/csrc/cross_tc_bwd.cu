@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       Cursor c;
-      for (c.start(a, t, 0); c.valid(t); c.advance(a, t, 0), ++g) {
+      for (c.start(a, t); c.valid(t); c.advance(a, t), ++g) {
         const Work& w = c.w;
-        const Work w1 = c.s == 0 ? decode(a, t, c.it, 1) : w;
         // the padding tile of an odd pair lies past the tokens and reads zeros
-        const int h1 = w1.real ? w1.h0 : 0, tok1 = w1.real ? w1.tok0 : a.n_q;
+        const RowTile r0 = row_tile(a, t, w, 0), r1 = row_tile(a, t, w, 1);
+        const int h1 = r1.real ? r1.h0 : 0, tok1 = r1.real ? r1.tok0 : a.n_q;
         if (++kv == t.hold_load && blockIdx.x == 0) break;      // test hook: a copy that never lands
         const int ks = g & 1;
         if (!load(L::kKEmpty + ks, L::kKFull + ks, g >> 1, L::kK + ks * L::kTile, &maps.k, w.hk * t.step_kh,
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         ++nk;
         if (c.s == 0) {
-          if (!load(L::kQEmpty, L::kQFull, nq[0], L::kQ, &maps.q, w.h0 * t.step_qh, w.tok0, w.b * t.step_qb)) break;
+          if (!load(L::kQEmpty, L::kQFull, nq[0], L::kQ, &maps.q, r0.h0 * t.step_qh, r0.tok0, w.b * t.step_qb)) break;
           ++nq[0];
           if (!load(L::kQEmpty + 1, L::kQFull + 1, nq[1], L::kQ + L::kTile, &maps.q, h1 * t.step_qh, tok1,
                     w.b * t.step_qb))
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!load(L::kVEmpty, L::kVFull, g, L::kV, &maps.v, w.hk * t.step_vh, (w.kt + c.s) * 128, w.b * t.step_vb)) break;
         ++nv;
         if (c.s == 0) {
-          if (!load(L::kOEmpty, L::kOFull, no[0], L::kDo, &maps.d_o, w.h0 * t.step_oh, w.tok0, w.b * t.step_ob)) break;
+          if (!load(L::kOEmpty, L::kOFull, no[0], L::kDo, &maps.d_o, r0.h0 * t.step_oh, r0.tok0, w.b * t.step_ob)) break;
           ++no[0];
           if (!load(L::kOEmpty + 1, L::kOFull + 1, no[1], L::kDo + L::kTile, &maps.d_o, h1 * t.step_oh, tok1,
                     w.b * t.step_ob))
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       Cursor c;
-      c.start(a, t, 0);
+      c.start(a, t);
       bool ok = true;
       if (c.valid(t)) ok = score(c, 0, 0) && score(c, 0, 1);
       for (int g = 0; ok && c.valid(t); ++g) {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         Cursor next = c;
-        next.advance(a, t, 0);
+        next.advance(a, t);
         if (last) ++items;      // Q buffers of the next item
 #pragma unroll
         for (int x = 0; x < 2 && ok; ++x) {
@@ -230,16 +230,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // times 0: warps 10 and 11 write zeros over those rows, 64 rows each.
       Cursor c;
       int g = 0;
-      for (c.start(a, t, 0); c.valid(t); c.advance(a, t, 0), ++g) {
-        const int j0 = (c.w.kt + c.s) * 128, keys = cross_keys(a, c.w.b), ks = g & 1;
-        const bool hidden = a.key_mask != nullptr || j0 + 128 > keys;
-        uint4 m;
-        if (hidden) m = seen_bits(a, c.w.b, j0, keys, lane);
+      for (c.start(a, t); c.valid(t); c.advance(a, t), ++g) {
+        const int j0 = (c.w.kt + c.s) * 128 + 64 * (warp - 10), ks = g & 1;
+        const uint32_t hidden0 = ~seen_word(a, c.w.b, j0, c.w.keys, lane), hidden1 = ~seen_word(a, c.w.b, j0 + 32, c.w.keys, lane);
+        auto clean = [&](uint8_t* tile) {
+          tile += 64 * (warp - 10) * 128;
+          if (hidden0) zero_rows<HD>(tile, 128 * 128, hidden0, lane);
+          if (hidden1) zero_rows<HD>(tile + 32 * 128, 128 * 128, hidden1, lane);
+        };
         if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kKFull + ks), (g >> 1) & 1, abort, lim))) break;
-        if (hidden) zero_hidden_rows<HD>(sm + L::kK + ks * L::kTile, m, 2 * (warp - 10), lane);
+        clean(sm + L::kK + ks * L::kTile);
         if (lane == 0) mbar_arrive(bar(L::kKClean + ks));
         if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kVFull), g & 1, abort, lim))) break;
-        if (hidden) zero_hidden_rows<HD>(sm + L::kV, m, 2 * (warp - 10), lane);
+        clean(sm + L::kV);
         if (lane == 0) mbar_arrive(bar(L::kVClean));
       }
     }
@@ -258,19 +261,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, abort, lim)) != 0;
     };
     for (int it = blockIdx.x; it < t.items && ok; it += gridDim.x) {
-      const Work w = decode(a, t, it, x);
-      const int keys = cross_keys(a, w.b);
+      const Work w = decode(a, t, it);
+      const RowTile q = row_tile(a, t, w, x);
       float nl = -INFINITY, nd = 0.f;     // -lse (log2 units) and -delta of the row
-      if (w.real) {
-        nl = __ldg(a.stats + (long long)w.row_tile * 256 + r);
-        nd = __ldg(a.stats + (long long)w.row_tile * 256 + 128 + r);
+      if (q.real) {
+        nl = __ldg(a.stats + (long long)q.at * 256 + r);
+        nd = __ldg(a.stats + (long long)q.at * 256 + 128 + r);
       }
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       for (int s = 0; s < w.n; ++s, ++g) {
         const int j0 = (w.kt + s) * 128;
-        const bool partial = a.key_mask != nullptr || j0 + 128 > keys;
-        uint4 mw;
-        if (partial) mw = seen_bits(a, w.b, j0, keys, lane);
+        const bool partial = a.key_mask != nullptr || j0 + 128 > w.keys;
+        uint32_t w4[4];
+        if (partial) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w4[i] = seen_word(a, w.b, j0 + 32 * i, w.keys, lane);
+        }
         if (!wait(L::kS + x, g)) { ok = false; break; }
         tc_fence_after();
         uint32_t p[128];
@@ -292,10 +298,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           p[2 * c + 1] = __float_as_uint(fast_ex2(e.y));
         }
         if (partial) {
-          const uint32_t w4[4] = {mw.x, mw.y, mw.z, mw.w};
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!((w4[c >> 5] >> (c & 31)) & 1u)) p[c] = 0u;
+          for (int i = 0; i < 4; ++i) {
+            if (w4[i] == 0xffffffffu) continue;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((w4[i] >> c) & 1u)) p[32 * i + c] = 0u;
+          }
         }
         if (!wait(L::kDp + x, g)) { ok = false; break; }
         tc_fence_after();
@@ -327,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++items;
       }
-      const int n = w.tok0 + rt, h = w.h0 + rg;
-      const bool row = w.real && n < a.n_q;
+      const int n = q.tok0 + rt, h = q.h0 + rg;
+      const bool row = q.real && n < a.n_q;
       const long long at = ((long long)w.b * a.heads + h) * a.n_q + n;
       if (a.splits > 1 || w.n == 0) {
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += 32) {
           uint32_t o[32];
           if (w.n > 0) {
@@ -348,16 +357,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // every MMA that reads the stream's dO is done: its place serves the
         // stores, and only then takes the next item's
-#pragma unroll
+        uint8_t* stage = sm + L::kDo + x * L::kTile + (warp & 3) * (L::kTile / 4);
+#pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += 64) {
           uint32_t o[64];
           TMEM_LD32(tQ + c0, (o + 0));
           TMEM_LD32(tQ + c0 + 32, (o + 32));
           TMEM_LD_WAIT((o + 0));
           TMEM_LD_WAIT((o + 32));
-          store_rows64(a, t, &maps.out, a.dq, w, sm + L::kDo + x * L::kTile + (warp & 3) * (L::kTile / 4) + c0 * 64,
-                       (warp & 3) * 32, c0, o, a.scale, lane);
+          stage_rows64(stage + c0 * 64, o, a.scale, lane);
         }
+        store_rows<HD>(a, t, &maps.out, a.dq, w.b, q, stage, (warp & 3) * 32, lane);
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
       }
