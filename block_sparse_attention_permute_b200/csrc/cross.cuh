@@ -72,7 +72,8 @@ cudaError_t launch_cross_tc_dq(const CrossArgs& a, const CrossTiles& t, const Cr
 cudaError_t launch_cross_tc_dkv(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st);
 cudaError_t launch_cross_stats(const CrossArgs& a, const CrossTiles& t, int D, cudaStream_t st);
 // cross_simt.cu (fp32)
-constexpr int kCrossSimtTile = 64;   // rows and keys of a tile
+constexpr int kCrossSimtRows = 64, kCrossSimtKeys = 32;       // tile of the forward and dQ
+constexpr int kCrossSimtKvRows = 32, kCrossSimtKvKeys = 64;   // tile of dK and dV
 cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, cudaStream_t st);
 cudaError_t launch_cross_simt_dq(const CrossArgs& a, int D, cudaStream_t st);
 cudaError_t launch_cross_simt_dkv(const CrossArgs& a, int D, cudaStream_t st);

@@ -107,6 +107,22 @@ void plan_tc(bsa_cross_s* c) {
   c->dkv_splits = (c->bwd.tiles + c->dkv_len - 1) / c->dkv_len;
 }
 
+// The splits of the fp32 kernels: three CTAs of the forward and two of the others
+// share an SM, and while fewer are left each runs faster.
+void plan_simt(bsa_cross_s* c) {
+  const long long bh = (long long)c->B * c->heads_kv, rows = (long long)(c->heads / c->heads_kv) * c->n_q;
+  const long long row_tiles = (rows + bsa::kCrossSimtRows - 1) / bsa::kCrossSimtRows;
+  const long long kv_rows = (rows + bsa::kCrossSimtKvRows - 1) / bsa::kCrossSimtKvRows;
+  const long long key_tiles = (c->n_kv + bsa::kCrossSimtKeys - 1) / bsa::kCrossSimtKeys;
+  c->fwd_len = split_units(row_tiles * bh, key_tiles, 3 * kSms, 1.0, 2.0);
+  c->fwd_splits = (int)((key_tiles + c->fwd_len - 1) / c->fwd_len);
+  c->dq_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 1.0, 2.0);
+  c->dq_splits = (int)((key_tiles + c->dq_len - 1) / c->dq_len);
+  const long long kv_tiles = (c->n_kv + bsa::kCrossSimtKvKeys - 1) / bsa::kCrossSimtKvKeys;
+  c->dkv_len = split_units(kv_tiles * bh, kv_rows, 2 * kSms, 1.0, 2.0);
+  c->dkv_splits = (int)((kv_rows + c->dkv_len - 1) / c->dkv_len);
+}
+
 // Map (d, head, token, batch) of a [B, n, heads, D] bf16 view with a box of 64
 // elements x `pack` heads x `tokens` tokens.  An axis that the view repeats
 // (stride 0) becomes one of length 1, its coordinate then stays 0.
@@ -235,18 +251,8 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   const double sc = scale > 0.0 ? scale : 1.0 / std::sqrt((double)head_dim);
   c.scale = (float)sc;
   c.scale_log2 = (float)(sc * 1.4426950408889634);
-  const long long kT = bsa::kCrossSimtTile, bh = (long long)batch * heads_kv;
-  const long long row_tiles = ((long long)(heads / heads_kv) * n_q + kT - 1) / kT, key_tiles = (n_kv + kT - 1) / kT;
-  if (dtype == BSA_BF16) {
-    plan_tc(&c);
-  } else {
-    c.fwd_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 0.5, 1.0);
-    c.fwd_splits = (int)((key_tiles + c.fwd_len - 1) / c.fwd_len);
-    c.dq_len = split_units(row_tiles * bh, key_tiles, kSms, 1.0, 1.0);
-    c.dq_splits = (int)((key_tiles + c.dq_len - 1) / c.dq_len);
-    c.dkv_len = split_units(key_tiles * bh, row_tiles, kSms, 1.0, 1.0);
-    c.dkv_splits = (int)((row_tiles + c.dkv_len - 1) / c.dkv_len);
-  }
+  if (dtype == BSA_BF16) plan_tc(&c);
+  else plan_simt(&c);
   cudaError_t e = cudaGetDevice(&c.device);
   if (e != cudaSuccess) return cuda_fail(e);
   if ((e = cudaMalloc(&c.d_status, sizeof(int32_t))) != cudaSuccess) return cuda_fail(e);
