@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsa.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["permute.cu", "select.cu", "pair.cu", "attn.cu", "api.cu", "select_static.cu", "rotary.cu",
-           "cross_api.cu", "cross_aux.cu", "cross_simt.cu", "cross_tc.cu",
+           "cross_api.cu", "cross_aux.cu", "cross_f32.cu", "cross_tc.cu",
            "cross_tc_bwd.cu"]
 HEADERS = ["common.cuh", "kernels.cuh", "views.cuh", "cross.cuh", "cross_tc.cuh"]
 

@@ -71,12 +71,12 @@ cudaError_t launch_cross_tc_forward(const CrossArgs& a, const CrossTiles& t, con
 cudaError_t launch_cross_tc_dq(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st);
 cudaError_t launch_cross_tc_dkv(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st);
 cudaError_t launch_cross_stats(const CrossArgs& a, const CrossTiles& t, int D, cudaStream_t st);
-// cross_simt.cu (fp32)
-constexpr int kCrossSimtRows = 64, kCrossSimtKeys = 32;       // tile of the forward and dQ
-constexpr int kCrossSimtKvRows = 32, kCrossSimtKvKeys = 64;   // tile of dK and dV
-cudaError_t launch_cross_simt_forward(const CrossArgs& a, int D, cudaStream_t st);
-cudaError_t launch_cross_simt_dq(const CrossArgs& a, int D, cudaStream_t st);
-cudaError_t launch_cross_simt_dkv(const CrossArgs& a, int D, cudaStream_t st);
+// cross_f32.cu (fp32)
+constexpr int kCrossF32Rows = 64, kCrossF32Keys = 32;       // tile of the forward and dQ
+constexpr int kCrossF32KvRows = 32, kCrossF32KvKeys = 64;   // tile of dK and dV
+cudaError_t launch_cross_f32_forward(const CrossArgs& a, int D, cudaStream_t st);
+cudaError_t launch_cross_f32_dq(const CrossArgs& a, int D, cudaStream_t st);
+cudaError_t launch_cross_f32_dkv(const CrossArgs& a, int D, cudaStream_t st);
 // cross_aux.cu
 cudaError_t launch_cross_merge(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
 cudaError_t launch_cross_delta(const CrossArgs& a, int D, cudaStream_t st);   // fp32

@@ -107,19 +107,19 @@ void plan_tc(bsa_cross_s* c) {
   c->dkv_splits = (c->bwd.tiles + c->dkv_len - 1) / c->dkv_len;
 }
 
-// The splits of the fp32 kernels: three CTAs of the forward and two of the others
-// share an SM, and while fewer are left each runs faster.
-void plan_simt(bsa_cross_s* c) {
+// The splits of the fp32 kernels: three CTAs of the forward share an SM, two of the
+// others.
+void plan_f32(bsa_cross_s* c) {
   const long long bh = (long long)c->B * c->heads_kv, rows = (long long)(c->heads / c->heads_kv) * c->n_q;
-  const long long row_tiles = (rows + bsa::kCrossSimtRows - 1) / bsa::kCrossSimtRows;
-  const long long kv_rows = (rows + bsa::kCrossSimtKvRows - 1) / bsa::kCrossSimtKvRows;
-  const long long key_tiles = (c->n_kv + bsa::kCrossSimtKeys - 1) / bsa::kCrossSimtKeys;
-  c->fwd_len = split_units(row_tiles * bh, key_tiles, 3 * kSms, 1.0, 2.0);
+  const long long row_tiles = (rows + bsa::kCrossF32Rows - 1) / bsa::kCrossF32Rows;
+  const long long key_tiles = (c->n_kv + bsa::kCrossF32Keys - 1) / bsa::kCrossF32Keys;
+  c->fwd_len = split_units(row_tiles * bh, key_tiles, 3 * kSms, 1.0, 4.0);
   c->fwd_splits = (int)((key_tiles + c->fwd_len - 1) / c->fwd_len);
-  c->dq_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 1.0, 2.0);
+  c->dq_len = split_units(row_tiles * bh, key_tiles, 2 * kSms, 1.0, 3.0);
   c->dq_splits = (int)((key_tiles + c->dq_len - 1) / c->dq_len);
-  const long long kv_tiles = (c->n_kv + bsa::kCrossSimtKvKeys - 1) / bsa::kCrossSimtKvKeys;
-  c->dkv_len = split_units(kv_tiles * bh, kv_rows, 2 * kSms, 1.0, 2.0);
+  const long long kv_rows = (rows + bsa::kCrossF32KvRows - 1) / bsa::kCrossF32KvRows;
+  const long long kv_tiles = (c->n_kv + bsa::kCrossF32KvKeys - 1) / bsa::kCrossF32KvKeys;
+  c->dkv_len = split_units(kv_tiles * bh, kv_rows, 2 * kSms, 1.0, 3.0);
   c->dkv_splits = (int)((kv_rows + c->dkv_len - 1) / c->dkv_len);
 }
 
@@ -252,7 +252,7 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   c.scale = (float)sc;
   c.scale_log2 = (float)(sc * 1.4426950408889634);
   if (dtype == BSA_BF16) plan_tc(&c);
-  else plan_simt(&c);
+  else plan_f32(&c);
   cudaError_t e = cudaGetDevice(&c.device);
   if (e != cudaSuccess) return cuda_fail(e);
   if ((e = cudaMalloc(&c.d_status, sizeof(int32_t))) != cudaSuccess) return cuda_fail(e);
@@ -308,7 +308,7 @@ bsa_status bsa_cross_attention(bsa_cross_t p, const bsa_view_t* q, const bsa_vie
     if ((s = make_maps(p, a, false, &maps, &t)) != BSA_OK) return s;
     e = bsa::launch_cross_tc_forward(a, t, maps, p->D, st);
   } else {
-    e = bsa::launch_cross_simt_forward(a, p->D, st);
+    e = bsa::launch_cross_f32_forward(a, p->D, st);
   }
   if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_merge(a, p->D, is_bf16, st);
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
@@ -346,12 +346,12 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
   a.splits = p->dq_splits;
   a.split_len = p->dq_len;
   if (e == cudaSuccess)
-    e = is_bf16 ? bsa::launch_cross_tc_dq(a, t, maps, p->D, st) : bsa::launch_cross_simt_dq(a, p->D, st);
+    e = is_bf16 ? bsa::launch_cross_tc_dq(a, t, maps, p->D, st) : bsa::launch_cross_f32_dq(a, p->D, st);
   if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_sum_q(a, p->D, is_bf16, st);
   a.splits = p->dkv_splits;
   a.split_len = p->dkv_len;
   if (e == cudaSuccess)
-    e = is_bf16 ? bsa::launch_cross_tc_dkv(a, t, maps, p->D, st) : bsa::launch_cross_simt_dkv(a, p->D, st);
+    e = is_bf16 ? bsa::launch_cross_tc_dkv(a, t, maps, p->D, st) : bsa::launch_cross_f32_dkv(a, p->D, st);
   if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_reduce_kv(a, p->D, is_bf16, st);
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
 }
