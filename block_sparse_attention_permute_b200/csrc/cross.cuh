@@ -43,6 +43,21 @@ __device__ __forceinline__ int cross_keys(const CrossArgs& a, int b) {
   return c;
 }
 
+// Whether batch element b attends exactly one key (asked where they could all be in
+// one tile; whole warp).  Its P is 1 and its dS 0, exactly, which P from a rounded
+// lse would miss by an ulp.
+__device__ __forceinline__ bool one_key(const CrossArgs& a, int b, int keys) {
+  if (keys > 128) return false;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = 32 * i + (threadIdx.x & 31);
+    n += __popc(__ballot_sync(0xffffffffu, j < keys && (a.key_mask == nullptr ||
+                                                        __ldg(a.key_mask + (long long)b * a.n_kv + j) != 0)));
+  }
+  return n == 1;
+}
+
 // Schedule of the tensor-core kernels.  A query tile is 128 rows: `tokens`
 // tokens of `pack` heads that share a K/V head (few tokens: more heads, so that
 // fewer rows are empty), heads fastest.

@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(kThreads, 2) cross_f32_dq(CrossArgs a) {
   }
   float acc[D / 8][4];
   clear(acc);
-  const int t0 = blockIdx.y * a.split_len, t1 = min(tiles, t0 + a.split_len);
+  const bool one = one_key(a, b, keys);          // dS is 0
+  const int t0 = blockIdx.y * a.split_len, t1 = one ? 0 : min(tiles, t0 + a.split_len);
   for (int t = t0; t < t1; ++t) {
     const uint32_t seen = seen_bits(a, b, t * kKeys, keys);
     __syncthreads();
@@ -360,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_f32_dkv(CrossArgs a) {
   load_keys<D>(sV + 32 * row_floats<D>(), a.v, b, hk, j0 + 32, seen1);
   cp_async_commit();
   const uint32_t seen = (warp >= 2 ? seen1 : seen0) >> (16 * (warp & 1)) & 0xffffu;   // the warp's 16 keys
+  const bool one = one_key(a, b, keys);          // dS is 0
   float dk[D / 8][4], dv[D / 8][4];
   clear(dk);
   clear(dv);
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_f32_dkv(CrossArgs a) {
           grad_of(s[j][i], dp[j][i], (seen >> ((lane >> 2) + 8 * (i >> 1))) & 1u, s_lse2[c], s_delta[c], a.scale_log2);
         }
       sum_tile<D>(s, sO, lane, dv);
-      sum_tile<D>(dp, sQ, lane, dk);
+      if (!one) sum_tile<D>(dp, sQ, lane, dk);
     }
   }
   cp_async_wait<0>();

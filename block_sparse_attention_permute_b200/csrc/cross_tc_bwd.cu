@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl = __ldg(a.stats + (long long)q.at * 256 + r);
         nd = __ldg(a.stats + (long long)q.at * 256 + 128 + r);
       }
-      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+      const float2 nl2 = make_float2(nl, nl);
       for (int s = 0; s < w.n; ++s, ++g) {
         const int j0 = (w.kt + s) * 128;
         const bool partial = a.key_mask != nullptr || j0 + 128 > w.keys;
@@ -308,20 +308,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!wait(L::kDp + x, g)) { ok = false; break; }
         tc_fence_after();
+        if (w.n == 1 && a.splits == 1) {
+          // All keys are here, so delta is the sum of P dP in fp32, not that of dO
+          // with the rounded O: with few keys dP - delta cancels, and the rounding
+          // of O was the largest error of dQ and dK (0.6% with two keys, else 0.25).
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint32_t d[32];
+            TMEM_LD32(tS + 32 * y, d);
+            TMEM_LD_WAIT(d);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              sum = fma2(make_float2(__uint_as_float(p[32 * y + 2 * c]), __uint_as_float(p[32 * y + 2 * c + 1])),
+                         make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])), sum);
+          }
+          nd = -(sum.x + sum.y);
+          if (q.real) a.stats[(long long)q.at * 256 + 128 + r] = nd;     // for dK
+          if (one_key(a, w.b, w.keys)) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) p[c] = 0u;
+          }
+        }
+        const float2 nd2 = make_float2(nd, nd);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[32];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int y = 0; y < 2; ++y) {
             uint32_t d[32];
-            TMEM_LD32(tS + 64 * h + 32 * q, d);
+            TMEM_LD32(tS + 64 * h + 32 * y, d);
             TMEM_LD_WAIT(d);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const int e = 64 * h + 32 * q + 2 * c;
+              const int e = 64 * h + 32 * y + 2 * c;
               const float2 v = mul2(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])),
                                     add2(make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])), nd2));
-              pk[16 * q + c] = pack_bf16x2(v.x, v.y);
+              pk[16 * y + c] = pack_bf16x2(v.x, v.y);
             }
           }
           TMEM_ST32(tS + 32 * h, pk);     // columns that this row has read
@@ -511,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     bool seen = j < keys;
     if (seen && a.key_mask) seen = __ldg(a.key_mask + (long long)b * a.n_kv + j) != 0;
+    const bool one = one_key(a, b, keys), flat = !seen || one;      // dS of the key is 0
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
     auto wait = [&](int y, int phase) {
@@ -571,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[16 * h + 2 * c + 1] = pack_bf16x2(v1.x, v1.y);
         }
       }
-      if (!seen) {
+      if (flat) {
 #pragma unroll
         for (int c = 0; c < 32; ++c) pk[c] = 0u;
       }

@@ -227,6 +227,24 @@ def test_shared_states_of_a_broadcast_batch(dev):
             check(name, x, ref[name])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["none", "length", "one"])
+def test_one_key_has_no_gradient_of_its_logit(kind, dtype, dev):
+    # softmax over one key is 1 whatever its logit: O = V, dQ = dK = 0 exactly
+    B, n_q, n_kv, H, D = 2, 130, 1 if kind == "none" else 40, 2, 64
+    op = bsa.CrossAttention(B, n_q, n_kv, H, H, D, dtype, device=dev)
+    q, d_o = rand((B, n_q, H, D), dtype, dev, 1, 3.0), rand((B, n_q, H, D), dtype, dev, 4)
+    k, v = rand((B, n_kv, H, D), dtype, dev, 2), rand((B, n_kv, H, D), dtype, dev, 3)
+    m = {"kv_len": torch.ones(B, dtype=torch.int32, device=dev)} if kind == "length" else \
+        masks(kind, B, n_kv, dev) if kind == "one" else {}
+    o, lse = op.forward(q, k, v, return_lse=True, **m)
+    ref = oracle(q, k, v, d_o, **m)
+    check("o", o, ref["o"])
+    dq, dk, dv = op.backward(d_o, q, k, v, o, lse, **m)
+    assert not dq.any() and not dk.any()
+    check("dv", dv, ref["dv"])
+
+
 @pytest.mark.parametrize("scale", [0.02, 1.5])
 def test_scale_and_peaked_rows(scale, dev):
     B, n_q, n_kv, H, D = 1, 100, 150, 2, 64
