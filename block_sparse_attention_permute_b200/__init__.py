@@ -13,6 +13,7 @@ and ``Plan.forward`` (all four in sequence).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -185,12 +186,37 @@ def _check_view(t, shape, dtype, device, name):
 
 def _views(*tensors):
     """One bsa_view_t per tensor (None: zeros) and their addresses (None: NULL)."""
-    flat = []
+    flat = array.array("q")
     for t in tensors:
-        flat += (0, 0, 0, 0) if t is None else (t.data_ptr(), *t.stride()[:3])
-    arr = (ctypes.c_longlong * len(flat))(*flat)
-    base = ctypes.addressof(arr)
-    return arr, [None if t is None else base + 32 * i for i, t in enumerate(tensors)]
+        if t is None:
+            flat.extend((0, 0, 0, 0))
+        else:
+            b, n, h, _ = t.stride()
+            flat.extend((t.data_ptr(), b, n, h))
+    base = flat.buffer_info()[0]
+    return flat, [None if t is None else base + 32 * i for i, t in enumerate(tensors)]
+
+
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _call(device, fn, *args):
+    """fn(*args, the current stream of `device`) with that device current."""
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+
+
+def _indexed(device):
+    """`device` with its index (of the current device where it has none)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
 
 
 def _triple(x, kind=float):
@@ -554,7 +580,7 @@ class Rope:
         c = RopeConfig((ctypes.c_int * 3)(*dims), _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling],
                        float(theta), (ctypes.c_double * 3)(*factor), (ctypes.c_double * 3)(*orig_len),
                        float(beta_fast), float(beta_slow), float(mscale), int(heads_k or 0))
-        self.device, self.dtype = plan.device, plan.dtype
+        self.device, self.dtype = _indexed(plan.device), plan.dtype
         self.q_shape = torch.Size(plan.orig_shape)
         self.k_shape = torch.Size((i.batch, i.n_tot, heads_k or i.heads, i.head_dim))
         self._h = ctypes.c_void_p()
@@ -588,17 +614,16 @@ class Rope:
                                      not t_origin.is_contiguous()):
             raise BsaError(1, f"t_origin must be an int64 tensor of shape {tuple(self.q_shape[:1])} on {dev}")
         if out is None:
-            qo = torch.empty(self.q_shape, dtype=dt, device=dev)
-            ko = None if k is None else torch.empty(self.k_shape, dtype=dt, device=dev)
+            qo = _like(q)
+            ko = None if k is None else _like(k)
         else:
             qo, ko = out if k is not None else (out, None)
             _check_view(qo, self.q_shape, dt, dev, "q_out")
             if k is not None:
                 _check_view(ko, self.k_shape, dt, dev, "k_out")
         keep, v = _views(q, k, qo, ko)
-        with torch.cuda.device(dev):
-            _check(load().bsa_rotary(self._h, *v, None if t_origin is None else t_origin.data_ptr(),
-                                     backward, _stream(dev)))
+        _call(dev, load().bsa_rotary, self._h, *v, None if t_origin is None else t_origin.data_ptr(),
+              backward)
         return qo if k is None else (qo, ko)
 
 
@@ -613,8 +638,7 @@ class CrossAttention:
         L = load()
         if dtype not in _DT:
             raise BsaError(1, f"dtype must be float32 or bfloat16, got {dtype}")
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
-            else torch.device(device)
+        self.device = _indexed(device)
         if self.device.type != "cuda":
             raise BsaError(1, "libbsa runs on CUDA devices only")
         if scale is not None and not scale > 0.0:
@@ -674,18 +698,16 @@ class CrossAttention:
         self._view(k, True, "k")
         self._view(v, True, "v")
         if out is None:
-            out = torch.empty(self.q_shape, dtype=self.dtype, device=self.device)
+            out = _like(q)
         else:
             self._view(out, False, "o")
         lse = torch.empty(self.lse_shape, dtype=torch.float32, device=self.device) if return_lse else None
         keep, views = _views(q, k, v, out)
         masks = self._masks(kv_len, key_mask)
         ws, keep_ws = self._workspace(workspace, self.forward_ws)
-        with torch.cuda.device(self.device):
-            _check(load().bsa_cross_attention(self._h, *views[:3], *masks, views[3],
-                                              None if lse is None else lse.data_ptr(), *ws,
-                                              None if dev_status is None else dev_status.data_ptr(),
-                                              _stream(self.device)))
+        _call(self.device, load().bsa_cross_attention, self._h, *views[:3], *masks, views[3],
+              None if lse is None else lse.data_ptr(), *ws,
+              None if dev_status is None else dev_status.data_ptr())
         return (out, lse) if return_lse else out
 
     def backward(self, d_o, q, k, v, o, lse, kv_len=None, key_mask=None, out=None, workspace=None,
@@ -697,8 +719,7 @@ class CrossAttention:
             self._view(t, kv, name)
         self._lse(lse)
         if out is None:
-            out = tuple(torch.empty(s, dtype=self.dtype, device=self.device)
-                        for s in (self.q_shape, self.kv_shape, self.kv_shape))
+            out = (_like(q), _like(k), _like(v))
         else:
             for t, kv, name in zip(out, (False, True, True), ("dq", "dk", "dv")):
                 self._view(t, kv, name)
@@ -706,16 +727,13 @@ class CrossAttention:
         keep, views = _views(q, k, v, o, d_o, dq, dk, dv)
         masks = self._masks(kv_len, key_mask)
         ws, keep_ws = self._workspace(workspace, self.backward_ws)
-        with torch.cuda.device(self.device):
-            _check(load().bsa_cross_attention_backward(
-                self._h, *views[:3], *masks, views[3], lse.data_ptr(), *views[4:], *ws,
-                None if dev_status is None else dev_status.data_ptr(), _stream(self.device)))
+        _call(self.device, load().bsa_cross_attention_backward, self._h, *views[:3], *masks, views[3],
+              lse.data_ptr(), *views[4:], *ws, None if dev_status is None else dev_status.data_ptr())
         return dq, dk, dv
 
     def check_status(self):
         """Synchronise the current stream and raise if a kernel recorded an error."""
-        with torch.cuda.device(self.device):
-            _check(load().bsa_cross_check_status(self._h, _stream(self.device)))
+        _call(self.device, load().bsa_cross_check_status, self._h)
 
     def set_watchdog(self, wait_limit_cycles=0, withhold_copy=0):
         """Bound of the tensor-core kernels' waits (0 = default, about a second) and the timeout

@@ -79,16 +79,20 @@ struct CrossMaps {
   CUtensorMap q, k, v, d_o, out;   // out: o of the forward, dq of the backward
 };
 
+// The prepare functions run once per device before a kernel's first launch.
 // cross_tc.cu (bf16)
+cudaError_t prepare_cross_tc_forward(const CrossTiles& t, int D);
 cudaError_t launch_cross_tc_forward(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D,
                                     cudaStream_t st);
 // cross_tc_bwd.cu (bf16; tiles with pack * tokens == 128)
+cudaError_t prepare_cross_tc_backward(int D);
 cudaError_t launch_cross_tc_dq(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st);
 cudaError_t launch_cross_tc_dkv(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st);
 cudaError_t launch_cross_stats(const CrossArgs& a, const CrossTiles& t, int D, cudaStream_t st);
 // cross_f32.cu (fp32)
 constexpr int kCrossF32Rows = 64, kCrossF32Keys = 32;       // tile of the forward and dQ
 constexpr int kCrossF32KvRows = 32, kCrossF32KvKeys = 64;   // tile of dK and dV
+cudaError_t prepare_cross_f32(int D);
 cudaError_t launch_cross_f32_forward(const CrossArgs& a, int D, cudaStream_t st);
 cudaError_t launch_cross_f32_dq(const CrossArgs& a, int D, cudaStream_t st);
 cudaError_t launch_cross_f32_dkv(const CrossArgs& a, int D, cudaStream_t st);

@@ -34,14 +34,17 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 // shortens the call: `slots` CTAs run at a time, each costs about `start` units
 // beside its work (its loads before the first product, its stores after the
 // last), and a split call about `extra` units more, for writing and merging the
-// partials.  Returns the units per split, *cost its estimate.
-int split_units(long long ctas, long long units, int slots, double start, double extra, double* cost = nullptr) {
+// partials.  Of the splits within `slack` of the least estimate the finest is
+// taken.  Returns the units per split, *cost its estimate.
+int split_units(long long ctas, long long units, int slots, double start, double extra, double* cost = nullptr,
+                double slack = 1.0) {
   long long len = units;
   double best = (double)((ctas + slots - 1) / slots) * (units + start);
   for (int s = 2; s <= 128 && s <= units; ++s) {
     const long long l = (units + s - 1) / s, n = (units + l - 1) / l;
     const double c = (double)((ctas * n + slots - 1) / slots) * (l + start) + extra;
     if (c < best) best = c, len = l;
+    else if (c <= slack * best) len = l;
   }
   if (cost) *cost = best;
   return (int)len;
@@ -103,7 +106,9 @@ void plan_tc(bsa_cross_s* c) {
   c->dq_len = split_units(bh * pairs, key_tiles, kSms, 1.0, 2.0);
   c->dq_splits = (key_tiles + c->dq_len - 1) / c->dq_len;
   plan_items(c, pairs, c->dq_splits, &c->bwd);
-  c->dkv_len = split_units(bh * key_tiles, c->bwd.tiles, kSms, 3.0, 2.0);
+  // (a CTA whose keys are past its batch element's has nothing to do: finer splits
+  // let others take its SM)
+  c->dkv_len = split_units(bh * key_tiles, c->bwd.tiles, kSms, 3.0, 2.0, nullptr, 1.06);
   c->dkv_splits = (c->bwd.tiles + c->dkv_len - 1) / c->dkv_len;
 }
 
@@ -255,7 +260,10 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   else plan_f32(&c);
   cudaError_t e = cudaGetDevice(&c.device);
   if (e != cudaSuccess) return cuda_fail(e);
-  if ((e = cudaMalloc(&c.d_status, sizeof(int32_t))) != cudaSuccess) return cuda_fail(e);
+  e = dtype == BSA_F32 ? bsa::prepare_cross_f32(head_dim) : bsa::prepare_cross_tc_forward(c.fwd, head_dim);
+  if (e == cudaSuccess && dtype == BSA_BF16) e = bsa::prepare_cross_tc_backward(head_dim);
+  if (e == cudaSuccess) e = cudaMalloc(&c.d_status, sizeof(int32_t));
+  if (e != cudaSuccess) return cuda_fail(e);
   if ((e = cudaMemset(c.d_status, 0, sizeof(int32_t))) != cudaSuccess ||
       (e = cudaStreamSynchronize(nullptr)) != cudaSuccess) {
     cudaFree(c.d_status);

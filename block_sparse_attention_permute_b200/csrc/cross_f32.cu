@@ -4,9 +4,10 @@
 //   O  = softmax(S) V
 //   P  = exp(S - L),  dP = dO V^T,  D = rowsum(dO * O),  dS = P * (dP - D)
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
-// Products run on the tensor cores in tf32, three for one: with x = h + l, h the
-// upper 11 bits of x's significand and l the rest, a b = ha hb + ha lb + la hb up
-// to 2^-21 of its size (la lb, and what tf32 drops of l), every sum in fp32.  The
+// Products run on the tensor cores in tf32, three for one: with x = h + l, h the 11
+// leading bits that tf32 keeps, a b = ha hb + ha lb + la hb up to 2^-20 of its size
+// (la lb, and what tf32 drops of l), every sum in fp32; the small products of a
+// tile have a sum of their own, as the tensor core rounds each addition to zero.  The
 // legacy warp MMA serves here: tcgen05 would want both parts of both operands in
 // shared memory, 256 KB for one pair of 128 x 128 tiles.  A warp owns 16 rows of
 // the result (query rows; keys for dK and dV) and keeps its logits, probabilities
@@ -67,7 +68,7 @@ __device__ __forceinline__ uint32_t seen_bits(const CrossArgs& a, int b, int j0,
   return __ballot_sync(0xffffffffu, s);
 }
 
-// x = hi + lo, both with the 11 leading bits that tf32 keeps (lo: nearly).
+// x = hi + lo, hi the 11 leading bits that tf32 keeps.
 __device__ __forceinline__ void split(uint32_t x, uint32_t& hi, uint32_t& lo) {
   hi = x & 0xffffe000u;
   lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
@@ -89,7 +90,7 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// c += a b for operands given as fp32: the small products first.
+// c + small += a b for operands given as fp32.
 struct Split4 {
   uint32_t hi[4], lo[4];
 };
@@ -99,12 +100,12 @@ __device__ __forceinline__ Split4 split4(const uint32_t (&x)[4]) {
   for (int i = 0; i < 4; ++i) split(x[i], s.hi[i], s.lo[i]);
   return s;
 }
-__device__ __forceinline__ void mma3(float (&c)[4], const Split4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma3(float (&c)[4], float (&small)[4], const Split4& a, uint32_t b0, uint32_t b1) {
   uint32_t h0, l0, h1, l1;
   split(b0, h0, l0);
   split(b1, h1, l1);
-  mma_tf32(c, a.lo, h0, h1);
-  mma_tf32(c, a.hi, l0, l1);
+  mma_tf32(small, a.lo, h0, h1);
+  mma_tf32(small, a.hi, l0, l1);
   mma_tf32(c, a.hi, h0, h1);
 }
 
@@ -113,10 +114,11 @@ __device__ __forceinline__ void mma3(float (&c)[4], const Split4& a, uint32_t b0
 // the same columns.
 template <int D>
 __device__ __forceinline__ void dot_tile(const float* A, const float* B, int lane, float (&s)[4][4]) {
+  float small[4][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+    for (int i = 0; i < 4; ++i) s[j][i] = small[j][i] = 0.f;
   // ldmatrix: lanes 8 m .. 8 m + 7 give the rows of matrix m
   const uint32_t pa = smem_addr(A + (lane & 15) * row_floats<D>() + (lane >> 4) * 4);
   const uint32_t pb = smem_addr(B + ((lane & 7) + (lane >> 4) * 8) * row_floats<D>() + ((lane >> 3) & 1) * 4);
@@ -129,10 +131,14 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int lan
     for (int jj = 0; jj < 2; ++jj) {
       uint32_t y[4];
       ldmatrix4(y, pb + (jj * 16 * row_floats<D>() + k) * 4);
-      mma3(s[2 * jj], xa, y[0], y[1]);
-      mma3(s[2 * jj + 1], xa, y[2], y[3]);
+      mma3(s[2 * jj], small[2 * jj], xa, y[0], y[1]);
+      mma3(s[2 * jj + 1], small[2 * jj + 1], xa, y[2], y[3]);
     }
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[j][i] += small[j][i];
 }
 
 // acc[n] += P (16 rows, 32 columns held as dot_tile leaves them) times the 32 rows
@@ -140,15 +146,23 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int lan
 template <int D>
 __device__ __forceinline__ void sum_tile(const float (&p)[4][4], const float* B, int lane, float (&acc)[D / 8][4]) {
   const float* q = B + 2 * (lane & 3) * row_floats<D>() + (lane >> 2);
+  Split4 x[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t x[4] = {__float_as_uint(p[j][0]), __float_as_uint(p[j][2]), __float_as_uint(p[j][1]),
+    const uint32_t y[4] = {__float_as_uint(p[j][0]), __float_as_uint(p[j][2]), __float_as_uint(p[j][1]),
                            __float_as_uint(p[j][3])};
-    const Split4 xa = split4(x);
-    const float* b = q + 8 * j * row_floats<D>();
+    x[j] = split4(y);
+  }
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-      mma3(acc[n], xa, __float_as_uint(b[8 * n]), __float_as_uint(b[8 * n + row_floats<D>()]));
+  for (int n = 0; n < D / 8; ++n) {
+    float small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float* b = q + 8 * j * row_floats<D>() + 8 * n;
+      mma3(acc[n], small, x[j], __float_as_uint(b[0]), __float_as_uint(b[row_floats<D>()]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] += small[i];
   }
 }
 
@@ -410,27 +424,39 @@ __global__ void __launch_bounds__(kThreads, 2) cross_f32_dkv(CrossArgs a) {
   }
 }
 
+// The forward (0), dQ (1), or dK and dV (2).
 template <int D>
-cudaError_t run_f32(int which, const CrossArgs& a, cudaStream_t st) {
-  constexpr int kRow = row_floats<D>() * (int)sizeof(float);
-  const long long rows = (long long)a.group * a.n_q;
-  const unsigned row_tiles = (unsigned)((rows + kRows - 1) / kRows), bh = (unsigned)(a.B * a.heads_kv);
-  const unsigned key_tiles = (unsigned)((a.n_kv + kCrossF32KvKeys - 1) / kCrossF32KvKeys);
-  void (*kernel)(CrossArgs) = which == 0 ? cross_f32_forward<D> : which == 1 ? cross_f32_dq<D> : cross_f32_dkv<D>;
-  const int smem = kRow * (which == 0 ? kRows + 2 * kKeys : which == 1 ? 2 * (kRows + kKeys)
-                                                                      : 2 * (kCrossF32KvRows + kCrossF32KvKeys));
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kernel<<<dim3((which == 2 ? key_tiles : row_tiles) * bh, a.splits), kThreads, smem, st>>>(a);
-  return cudaGetLastError();
-}
+struct F32 {
+  static auto kernel(int which) {
+    return which == 0 ? cross_f32_forward<D> : which == 1 ? cross_f32_dq<D> : cross_f32_dkv<D>;
+  }
+  static int smem(int which) {
+    return row_floats<D>() * (int)sizeof(float) *
+           (which == 0 ? kRows + 2 * kKeys : 2 * (which == 1 ? kRows + kKeys : kCrossF32KvRows + kCrossF32KvKeys));
+  }
+  static cudaError_t run(int which, const CrossArgs& a, cudaStream_t st) {
+    const long long rows = (long long)a.group * a.n_q;
+    const unsigned row_tiles = (unsigned)((rows + kRows - 1) / kRows), bh = (unsigned)(a.B * a.heads_kv);
+    const unsigned key_tiles = (unsigned)((a.n_kv + kCrossF32KvKeys - 1) / kCrossF32KvKeys);
+    kernel(which)<<<dim3((which == 2 ? key_tiles : row_tiles) * bh, a.splits), kThreads, smem(which), st>>>(a);
+    return cudaGetLastError();
+  }
+  static cudaError_t prepare() {
+    for (int which = 0; which < 3; ++which) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel(which), cudaFuncAttributeMaxDynamicSharedMemorySize, smem(which));
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
+};
 
 cudaError_t run_f32(int which, const CrossArgs& a, int D, cudaStream_t st) {
-  return D == 128 ? run_f32<128>(which, a, st) : run_f32<64>(which, a, st);
+  return D == 128 ? F32<128>::run(which, a, st) : F32<64>::run(which, a, st);
 }
 
 }  // namespace
 
+cudaError_t prepare_cross_f32(int D) { return D == 128 ? F32<128>::prepare() : F32<64>::prepare(); }
 cudaError_t launch_cross_f32_forward(const CrossArgs& a, int D, cudaStream_t st) { return run_f32(0, a, D, st); }
 cudaError_t launch_cross_f32_dq(const CrossArgs& a, int D, cudaStream_t st) { return run_f32(1, a, D, st); }
 cudaError_t launch_cross_f32_dkv(const CrossArgs& a, int D, cudaStream_t st) { return run_f32(2, a, D, st); }

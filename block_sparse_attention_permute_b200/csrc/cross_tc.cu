@@ -425,10 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int HD, bool SHARED>
 cudaError_t launch(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, cudaStream_t st) {
-  const cudaError_t e = prepare_kernel(cross_tc_forward<HD, SHARED>, Layout<HD, SHARED>::kAlloc);
-  if (e != cudaSuccess) return e;
-  cross_tc_forward<HD, SHARED><<<t.items < t.ctas ? t.items : t.ctas, kThreads, Layout<HD, SHARED>::kAlloc, st>>>(a, t, m);
+  cross_tc_forward<HD, SHARED>
+      <<<t.items < t.ctas ? t.items : t.ctas, kThreads, Layout<HD, SHARED>::kAlloc, st>>>(a, t, m);
   return cudaGetLastError();
+}
+
+template <int HD, bool SHARED>
+cudaError_t prepare() {
+  return prepare_kernel(cross_tc_forward<HD, SHARED>, Layout<HD, SHARED>::kAlloc);
 }
 
 }  // namespace
@@ -437,6 +441,11 @@ cudaError_t launch_cross_tc_forward(const CrossArgs& a, const CrossTiles& t, con
                                     cudaStream_t st) {
   if (t.shared) return D == 128 ? launch<128, true>(a, t, m, st) : launch<64, true>(a, t, m, st);
   return D == 128 ? launch<128, false>(a, t, m, st) : launch<64, false>(a, t, m, st);
+}
+
+cudaError_t prepare_cross_tc_forward(const CrossTiles& t, int D) {
+  if (t.shared) return D == 128 ? prepare<128, true>() : prepare<64, true>();
+  return D == 128 ? prepare<128, false>() : prepare<64, false>();
 }
 
 }  // namespace bsa

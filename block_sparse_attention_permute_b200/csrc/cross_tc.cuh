@@ -216,10 +216,11 @@ __device__ __forceinline__ void store_rows(const CrossArgs& a, const CrossTiles&
   __syncwarp();
 }
 
-// Refuses to launch a build whose kernel does not get kRegsLaunch registers per
-// thread (the register split assumes it), and sets the shared-memory size.
+// Before the first launch on a device: refuses a build whose kernel does not get
+// kRegsLaunch registers per thread (the register split assumes it), and sets the
+// shared-memory size.
 template <class K>
-cudaError_t prepare_kernel(K kernel, int smem) {
+inline cudaError_t prepare_kernel(K kernel, int smem) {
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
   if (e != cudaSuccess) return e;

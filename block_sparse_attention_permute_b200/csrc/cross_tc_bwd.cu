@@ -689,19 +689,21 @@ __global__ void __launch_bounds__(256) cross_stats(const __grid_constant__ Cross
 
 template <int HD>
 cudaError_t launch_dq(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, cudaStream_t st) {
-  const cudaError_t e = prepare_kernel(cross_tc_dq<HD>, DqLayout<HD>::kAlloc);
-  if (e != cudaSuccess) return e;
   cross_tc_dq<HD><<<t.items < t.ctas ? t.items : t.ctas, kThreads, DqLayout<HD>::kAlloc, st>>>(a, t, m);
   return cudaGetLastError();
 }
 
 template <int HD>
 cudaError_t launch_dkv(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, cudaStream_t st) {
-  const cudaError_t e = prepare_kernel(cross_tc_dkv<HD>, DkvLayout<HD>::kAlloc);
-  if (e != cudaSuccess) return e;
   const unsigned ctas = (unsigned)(a.B * a.heads_kv * ((a.n_kv + 127) / 128) * a.splits);
   cross_tc_dkv<HD><<<ctas, kThreads, DkvLayout<HD>::kAlloc, st>>>(a, t, m);
   return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t prepare() {
+  const cudaError_t e = prepare_kernel(cross_tc_dq<HD>, DqLayout<HD>::kAlloc);
+  return e == cudaSuccess ? prepare_kernel(cross_tc_dkv<HD>, DkvLayout<HD>::kAlloc) : e;
 }
 
 }  // namespace
@@ -712,6 +714,7 @@ cudaError_t launch_cross_tc_dq(const CrossArgs& a, const CrossTiles& t, const Cr
 cudaError_t launch_cross_tc_dkv(const CrossArgs& a, const CrossTiles& t, const CrossMaps& m, int D, cudaStream_t st) {
   return D == 128 ? launch_dkv<128>(a, t, m, st) : launch_dkv<64>(a, t, m, st);
 }
+cudaError_t prepare_cross_tc_backward(int D) { return D == 128 ? prepare<128>() : prepare<64>(); }
 cudaError_t launch_cross_stats(const CrossArgs& a, const CrossTiles& t, int D, cudaStream_t st) {
   const long long rows = (long long)a.B * a.heads_kv * t.tiles * 128;
   const unsigned ctas = (unsigned)(rows * (D / 8) / 256);
