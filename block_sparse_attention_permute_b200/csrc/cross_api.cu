@@ -35,7 +35,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 // beside its work (its loads before the first product, its stores after the
 // last), and a split call about `extra` units more, for writing and merging the
 // partials.  Of the splits within `slack` of the least estimate the finest is
-// taken.  Returns the units per split, *cost its estimate.
+// taken that needs no more than four rounds of CTAs.  Returns the units per split, *cost its estimate.
 int split_units(long long ctas, long long units, int slots, double start, double extra, double* cost = nullptr,
                 double slack = 1.0) {
   long long len = units;
@@ -44,7 +44,7 @@ int split_units(long long ctas, long long units, int slots, double start, double
     const long long l = (units + s - 1) / s, n = (units + l - 1) / l;
     const double c = (double)((ctas * n + slots - 1) / slots) * (l + start) + extra;
     if (c < best) best = c, len = l;
-    else if (c <= slack * best) len = l;
+    else if (c <= slack * best && ctas * n <= 4ll * slots) len = l;
   }
   if (cost) *cost = best;
   return (int)len;
@@ -108,7 +108,7 @@ void plan_tc(bsa_cross_s* c) {
   plan_items(c, pairs, c->dq_splits, &c->bwd);
   // (a CTA whose keys are past its batch element's has nothing to do: finer splits
   // let others take its SM)
-  c->dkv_len = split_units(bh * key_tiles, c->bwd.tiles, kSms, 3.0, 2.0, nullptr, 1.06);
+  c->dkv_len = split_units(bh * key_tiles, c->bwd.tiles, kSms, 3.0, 2.0, nullptr, 1.07);
   c->dkv_splits = (c->bwd.tiles + c->dkv_len - 1) / c->dkv_len;
 }
 
@@ -192,6 +192,8 @@ bsa_status fill(const bsa_cross_s* p, const bsa_view_t* q, const bsa_view_t* k, 
   if ((s = bsa::check_view(o, "o", p->B, p->n_q, p->heads, p->D, esz, o_written, &a->o)) != BSA_OK) return s;
   if ((p->n_q > 1 && a->q.n == 0) || (p->n_kv > 1 && (a->k.n == 0 || a->v.n == 0)))
     return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no view that repeats its tokens (token stride 0)");
+  if (p->heads > 1 && a->q.h == 0)
+    return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no query or gradient that repeats its heads (head stride 0)");
   if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return fail(BSA_ERR_INVALID_ARG, "kv_len must be 4-byte aligned");
   a->kv_len = kv_len;
   a->key_mask = key_mask;
@@ -342,6 +344,8 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
   if ((s = check_ws(ws, ws_bytes, backward_bytes(p))) != BSA_OK) return s;
   if (p->n_q > 1 && a.d_o.n == 0)
     return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no view that repeats its tokens (token stride 0)");
+  if (p->heads > 1 && a.d_o.h == 0)
+    return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no query or gradient that repeats its heads (head stride 0)");
   const bool is_bf16 = p->dtype == BSA_BF16;
   a.lse = const_cast<float*>(lse);
   a.delta = a.stats = static_cast<float*>(ws);

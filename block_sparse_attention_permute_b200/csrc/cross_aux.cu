@@ -24,43 +24,52 @@ __device__ __forceinline__ void row_of(const CrossArgs& a, long long at, int& b,
 
 // One warp per row.  With partials (O_s, m_s, l_s) of the key splits:
 // M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s, and
-// lse = ln 2 (M + log2 sum w_s l_s).  The lanes first share the splits, then
-// the columns (D = 64: half a warp takes every other split); eight partial rows
-// are in flight, since few rows leave latency as the bound.  Every sum has a
-// fixed order.
+// lse = ln 2 (M + log2 sum w_s l_s).  A lane forms the weight of one split of 32,
+// then takes its columns (D = 64: half a warp every other split) of them all.  Few
+// rows leave latency as the bound, so sixteen partial rows are in flight, asked for
+// before their weights are known.  Every sum has a fixed order.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) cross_merge(CrossArgs a) {
-  constexpr int kHalves = 128 / D;
-  const long long rows = cross_rows(a), at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(128) cross_merge(CrossArgs a) {
+  constexpr int kHalves = 128 / D, kFlight = 16;
+  const long long rows = cross_rows(a), at = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (at >= rows) return;
   const int lane = threadIdx.x & 31, c = (lane % (D / 4)) * 4, first = lane / (D / 4);
-  float M = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, __ldg(a.part_ml + s * rows + at).x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float base = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  for (int s = lane; s < a.splits; s += 32) {
-    const float2 ml = __ldg(a.part_ml + s * rows + at);
-    l = fmaf(exp2f(ml.x - base), ml.y, l);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = first; s0 < a.splits; s0 += 8 * kHalves) {
-    float4 x[8];
-    float w[8];
+  for (int s32 = 0; s32 < a.splits; s32 += 32) {
+    const int mine = s32 + lane;
+    const float2 ml = mine < a.splits ? __ldg(a.part_ml + mine * rows + at) : make_float2(-INFINITY, 0.f);
+    float top = 0.f, w = 0.f;
+    for (int s0 = s32; s0 < min(s32 + 32, a.splits); s0 += kFlight * kHalves) {
+      float4 x[kFlight];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int s = s0 + u * kHalves;
-      // a split without keys (m = -inf, w = 0) has not written its O
-      w[u] = s < a.splits ? exp2f(__ldg(a.part_ml + s * rows + at).x - base) : 0.f;
-      x[u] = w[u] != 0.f ? in4(a.part_o + (s * rows + at) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < kFlight; ++u) {
+        const int s = s0 + u * kHalves + first;
+        x[u] = s < a.splits ? in4(a.part_o + (s * rows + at) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (s0 == s32) {
+        top = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, M);
+        const float base = top == -INFINITY ? 0.f : top, keep = exp2f(M - base);
+        w = exp2f(ml.x - base);
+        float sum = ml.x == -INFINITY ? 0.f : w * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = fmaf(l, keep, sum);
+        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+        M = top;
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int s = s0 + u * kHalves + first;
+        const float ws = __shfl_sync(0xffffffffu, w, s & 31);
+        if (s < a.splits && ws != 0.f)      // a split without keys (m = -inf, w = 0) has not written its O
+          acc = make_float4(fmaf(ws, x[u].x, acc.x), fmaf(ws, x[u].y, acc.y), fmaf(ws, x[u].z, acc.z),
+                            fmaf(ws, x[u].w, acc.w));
+      }
     }
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      acc = make_float4(fmaf(w[u], x[u].x, acc.x), fmaf(w[u], x[u].y, acc.y), fmaf(w[u], x[u].z, acc.z),
-                        fmaf(w[u], x[u].w, acc.w));
   }
   if (kHalves == 2) {
     acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
@@ -139,7 +148,7 @@ template <typename T, int D>
 cudaError_t run_aux(int which, const CrossArgs& a, cudaStream_t st) {
   const long long rows = cross_rows(a), keys = (long long)a.B * a.heads_kv * a.n_kv;
   const unsigned row_ctas = (unsigned)((rows + 1024 / D - 1) / (1024 / D));
-  if (which == 0) cross_merge<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
+  if (which == 0) cross_merge<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);
   else if (which == 1) cross_sum_q<T, D><<<row_ctas, 256, 0, st>>>(a);
   else cross_reduce_kv<T, D><<<dim3((unsigned)((keys * (D / 4) + 255) / 256), 2), 256, 0, st>>>(a);
   return cudaGetLastError();

@@ -11,8 +11,11 @@ Every other fp32 sum of n terms is within n 2^-24 of the sum of their magnitudes
   dS   off by  P t + |dS| (up + e),                t = errors of dP and of D = rowsum(dO O), where O
        comes rounded from the forward: 2^-23 D (|dO| |V|) + |dO| err(O) + D 2^-23 |dO| |O|
   dQ   off by  scale (errors of dS) |K| + n 2^-23 scale |dS| |K|, then u |dQ|;  dK alike.
+For fp32 a product is three tf32 products, within 2^-20 of its size: for a logit that is inside
+the D 2^-23 above (D >= 64), for the other products inside e >= 2^-20.
 """
 import math
+import random
 
 import pytest
 import torch
@@ -141,6 +144,10 @@ SHAPES = [
     (2, 1, 5001, 6, 2, 64, "holes"),
     (1, 17, 9000, 1, 1, 128, "both"),
     (4, 33, 40, 256, 1, 64, "length"),
+    (1, 1, 300, 127, 1, 64, "holes"),
+    (2, 2, 150, 96, 1, 128, "length"),
+    (3, 1, 1, 2, 1, 128, "none"),
+    (1, 3000, 129, 1, 1, 64, "empty"),
 ]
 IDS = ["x".join(map(str, s)) for s in SHAPES]
 
@@ -351,6 +358,93 @@ def test_writes_only_its_buffers(dev):
                 assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_sizes_views_and_masks(seed, dev):
+    rng = random.Random(seed)
+    dtype, D = rng.choice((torch.float32, torch.bfloat16)), rng.choice((64, 128))
+    B, hkv, G = rng.randint(1, 3), rng.choice((1, 2, 3)), rng.choice((1, 1, 2, 3, 5, 8))
+    n_q = rng.choice((1, 2, 7, 31, 128, 129, 260, 511))
+    n_kv = rng.choice((1, 2, 31, 64, 127, 128, 129, 383, 384, 385, 1500))
+    H = hkv * G
+
+    def view(n, heads, s, scale=1.0):
+        kind = rng.randint(0, 3)
+        x = rand((B, n, heads, D), dtype, dev, 100 * seed + s, scale)
+        if kind == 1:        # heads before tokens
+            return x.transpose(1, 2).contiguous().transpose(1, 2)
+        if kind == 2:        # every other head of a wider tensor, more tokens behind
+            wide = rand((B, n + 3, heads * 2, D), dtype, dev, 7)
+            wide[:, :n, ::2] = x
+            return wide[:, :n, ::2]
+        if kind == 3:        # the same for the whole batch
+            return x[:1].expand(B, -1, -1, -1)
+        return x
+
+    q, k, v, d_o = view(n_q, H, 1, 2.0), view(n_kv, hkv, 2), view(n_kv, hkv, 3), view(n_q, H, 4)
+    m = masks(rng.choice(("none", "length", "holes", "both", "empty")), B, n_kv, dev, seed)
+    op = bsa.CrossAttention(B, n_q, n_kv, H, hkv, D, dtype, device=dev)
+    ref = oracle(q, k, v, d_o, **m)
+    o, lse = op.forward(q, k, v, return_lse=True, **m)
+    check("o", o, ref["o"])
+    check("lse", lse, ref["lse"])
+    for name, x in zip(("dq", "dk", "dv"), op.backward(d_o, q, k, v, o, lse, **m)):
+        check(name, x, ref[name])
+    op.check_status()
+
+
+def test_two_objects_on_two_streams(dev):
+    # calls that overlap on the GPU, each with its own workspace
+    shapes = ((2, 300, 500, 4, 2, 128), (1, 1, 20000, 8, 2, 64))
+    for dtype in (torch.float32, torch.bfloat16):
+        streams = [torch.cuda.Stream(dev) for _ in shapes]
+        work = []
+        for i, s in enumerate(shapes):
+            B, n_q, n_kv, H, hkv, D = s
+            op = bsa.CrossAttention(*s, dtype, device=dev)
+            x = [rand(t, dtype, dev, 10 * i + j) for j, t in enumerate((op.q_shape, op.kv_shape, op.kv_shape, op.q_shape))]
+            o, lse = op.forward(*x[:3], return_lse=True)
+            work.append((op, x, o, lse, op.backward(x[3], *x[:3], o, lse)))
+        torch.cuda.synchronize()
+        got = [[], []]
+        for _ in range(3):
+            for i, st in enumerate(streams):
+                op, x, _, _, _ = work[i]
+                with torch.cuda.stream(st):
+                    o, lse = op.forward(*x[:3], return_lse=True)
+                    got[i].append((o, lse, *op.backward(x[3], *x[:3], o, lse)))
+        torch.cuda.synchronize()
+        for i in range(2):
+            for run in got[i]:
+                for a, b in zip(run, (work[i][2], work[i][3], *work[i][4])):
+                    assert torch.equal(a, b)
+
+
+def test_a_wait_that_runs_out_is_reported(dev):
+    # the first CTA leaves out its n-th K/V copy: the waits end at their limit, the call with a
+    # status, and the object works again afterwards
+    B, n_q, n_kv, H, D = 1, 300, 700, 2, 64
+    op = bsa.CrossAttention(B, n_q, n_kv, H, H, D, torch.bfloat16, device=dev)
+    q, d_o = rand((B, n_q, H, D), torch.bfloat16, dev, 1), rand((B, n_q, H, D), torch.bfloat16, dev, 4)
+    k, v = rand((B, n_kv, H, D), torch.bfloat16, dev, 2), rand((B, n_kv, H, D), torch.bfloat16, dev, 3)
+    length = torch.full((B,), n_kv - 1, dtype=torch.int32, device=dev)
+    o, lse = op.forward(q, k, v, kv_len=length, return_lse=True)
+    g = op.backward(d_o, q, k, v, o, lse, kv_len=length)
+    op.check_status()
+    for n in (1, 2):
+        op.set_watchdog(20_000_000, n)
+        for call in (lambda: op.forward(q, k, v, kv_len=length),
+                     lambda: op.backward(d_o, q, k, v, o, lse, kv_len=length)):
+            call()
+            with pytest.raises(bsa.BsaError, match="wait") as err:
+                op.check_status()
+            assert err.value.status == 4
+    op.set_watchdog()
+    assert torch.equal(op.forward(q, k, v, kv_len=length), o)
+    for x, y in zip(g, op.backward(d_o, q, k, v, o, lse, kv_len=length)):
+        assert torch.equal(x, y)
+    op.check_status()
+
+
 def test_refusals(dev):
     op = bsa.CrossAttention(1, 4, 3000, 2, 1, 64, torch.bfloat16, device=dev)
     q = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16, device=dev)
@@ -376,6 +470,13 @@ def test_refusals(dev):
         with pytest.raises(bsa.BsaError) as err:
             op.forward(q, k, k, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
         assert err.value.status == 5
+    for bad in ((q[:, :1].expand(-1, 4, -1, -1), k, k), (q, k[:, :1].expand(-1, 3000, -1, -1), k),
+                (q[:, :, :1].expand(-1, -1, 2, -1), k, k)):
+        with pytest.raises(bsa.BsaError, match="repeats") as err:
+            op.forward(*bad)
+        assert err.value.status == 2
+    with pytest.raises(bsa.BsaError, match="scale"):
+        bsa.CrossAttention(1, 4, 4, 2, 1, 64, scale=0.0)
     torch.cuda.synchronize()
 
 
