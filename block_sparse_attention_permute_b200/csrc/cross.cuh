@@ -23,6 +23,10 @@ struct CrossArgs {
   float2* part_ml;           // [splits, rows]
   // Row-split partials of dK and dV: [splits, 2, B, heads_kv, n_kv, D].
   float* part_kv;
+  // With the attended keys gathered (k and v then are copies without gaps, kv_len
+  // their counts, key_mask null): place of each key among them, -1 if none.  dK and
+  // dV then always go through part_kv.
+  int32_t* slot_of;          // [B, n_kv] or null
   int B, n_q, n_kv, heads, heads_kv, group;
   int splits;                // of the kernel at hand
   int split_len;             // key tiles or steps (forward, dQ) or row tiles (dK, dV) per split
@@ -97,6 +101,9 @@ cudaError_t launch_cross_f32_forward(const CrossArgs& a, int D, cudaStream_t st)
 cudaError_t launch_cross_f32_dq(const CrossArgs& a, int D, cudaStream_t st);
 cudaError_t launch_cross_f32_dkv(const CrossArgs& a, int D, cudaStream_t st);
 // cross_aux.cu
+// slot_of and counts [B] from kv_len and key_mask, then the copies of K and V.
+cudaError_t launch_cross_gather(const CrossArgs& a, int32_t* counts, void* k, void* v, int D, bool is_bf16,
+                                cudaStream_t st);
 cudaError_t launch_cross_merge(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);
 cudaError_t launch_cross_delta(const CrossArgs& a, int D, cudaStream_t st);   // fp32
 cudaError_t launch_cross_sum_q(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st);

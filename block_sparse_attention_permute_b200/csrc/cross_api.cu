@@ -21,6 +21,7 @@ struct bsa_cross_s {
   bsa::CrossTiles fwd, bwd;  // schedules of the forward, and of dQ (and the query tiles of dK, dV) (bf16)
   int fwd_splits, fwd_len;   // partials of a row in the forward, key tiles per split
   int dq_splits, dq_len;     // key splits of dQ
+  bool gathers;              // with a key mask, attended K and V rows are copied together first
   int dkv_splits, dkv_len;   // row splits of dK and dV, row tiles in each
 };
 
@@ -145,22 +146,55 @@ bsa_status make_map(CUtensorMap* m, const bsa::View& v, int B, int n, int heads,
 
 size_t rows_of(const bsa_cross_s* p) { return (size_t)p->B * p->heads * p->n_q; }
 
-size_t forward_bytes(const bsa_cross_s* p) {
-  if (p->fwd_splits == 1) return 0;
-  return round256((size_t)p->fwd_splits * rows_of(p) * p->D * sizeof(float)) +
-         round256((size_t)p->fwd_splits * rows_of(p) * sizeof(float2));
+// Where a call's workspace begins when it gathers keys: their places, the counts,
+// the copies of K and V.
+size_t kv_copy_bytes(const bsa_cross_s* p) {
+  return round256((size_t)p->B * p->n_kv * p->heads_kv * p->D * (p->dtype == BSA_BF16 ? 2 : 4));
+}
+size_t gather_bytes(const bsa_cross_s* p) {
+  if (!p->gathers) return 0;
+  return round256((size_t)p->B * p->n_kv * sizeof(int32_t)) + round256((size_t)p->B * sizeof(int32_t)) +
+         2 * kv_copy_bytes(p);
 }
 
-// Backward workspace: the row sums (with lse in the query tiles' order on the
-// tensor cores), then the partials of dQ, whose place those of dK and dV take.
+size_t forward_bytes(const bsa_cross_s* p) {
+  size_t n = gather_bytes(p);
+  if (p->fwd_splits > 1)
+    n += round256((size_t)p->fwd_splits * rows_of(p) * p->D * sizeof(float)) +
+         round256((size_t)p->fwd_splits * rows_of(p) * sizeof(float2));
+  return n;
+}
+
+// Backward workspace, after the gathered keys: the row sums (with lse in the query
+// tiles' order on the tensor cores), then the partials of dQ, whose place those of
+// dK and dV take.
 size_t stats_bytes(const bsa_cross_s* p) {
   return p->dtype == BSA_BF16 ? round256((size_t)p->B * p->heads_kv * p->bwd.tiles * 256 * sizeof(float))
                               : round256(rows_of(p) * sizeof(float));
 }
 size_t backward_bytes(const bsa_cross_s* p) {
   const size_t q = p->dq_splits > 1 ? (size_t)p->dq_splits * rows_of(p) : 0;
-  const size_t kv = p->dkv_splits > 1 ? (size_t)p->dkv_splits * 2 * p->B * p->heads_kv * p->n_kv : 0;
-  return stats_bytes(p) + round256((q > kv ? q : kv) * p->D * sizeof(float));
+  const size_t kv =
+      p->dkv_splits > 1 || p->gathers ? (size_t)p->dkv_splits * 2 * p->B * p->heads_kv * p->n_kv : 0;
+  return gather_bytes(p) + stats_bytes(p) + round256((q > kv ? q : kv) * p->D * sizeof(float));
+}
+
+// Copies the attended rows of K and V together at the start of `ws` and lets *a
+// read them there, without a mask.
+cudaError_t gather_keys(const bsa_cross_s* p, char* ws, bsa::CrossArgs* a, cudaStream_t st) {
+  a->slot_of = reinterpret_cast<int32_t*>(ws);
+  ws += round256((size_t)p->B * p->n_kv * sizeof(int32_t));
+  int32_t* counts = reinterpret_cast<int32_t*>(ws);
+  ws += round256((size_t)p->B * sizeof(int32_t));
+  char *k = ws, *v = ws + kv_copy_bytes(p);
+  const cudaError_t e = bsa::launch_cross_gather(*a, counts, k, v, p->D, p->dtype == BSA_BF16, st);
+  const long long h = p->heads_kv > 1 ? p->D : 0, n = p->n_kv > 1 ? (long long)p->heads_kv * p->D : 0;
+  const long long b = p->B > 1 ? (long long)p->n_kv * p->heads_kv * p->D : 0;
+  a->k = bsa::View{k, b, n, h};
+  a->v = bsa::View{v, b, n, h};
+  a->kv_len = counts;
+  a->key_mask = nullptr;
+  return e;
 }
 
 bsa_status check_cross(const bsa_cross_s* p) {
@@ -260,6 +294,9 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   c.scale_log2 = (float)(sc * 1.4426950408889634);
   if (dtype == BSA_BF16) plan_tc(&c);
   else plan_f32(&c);
+  // Gathering costs two launches and one more pass over K and V; with 2048 query
+  // rows or more to a K/V head that is less than the work on a masked key in ten.
+  c.gathers = (long long)(heads / heads_kv) * n_q >= 2048 && n_kv > 128;
   cudaError_t e = cudaGetDevice(&c.device);
   if (e != cudaSuccess) return cuda_fail(e);
   e = dtype == BSA_F32 ? bsa::prepare_cross_f32(head_dim) : bsa::prepare_cross_tc_forward(c.fwd, head_dim);
@@ -305,13 +342,14 @@ bsa_status bsa_cross_attention(bsa_cross_t p, const bsa_view_t* q, const bsa_vie
   a.splits = p->fwd_splits;
   a.split_len = p->fwd_len;
   if (a.splits > 1) {
-    a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) +
-                                          round256((size_t)a.splits * rows_of(p) * p->D * sizeof(float)));
+    char* parts = static_cast<char*>(ws) + gather_bytes(p);
+    a.part_o = reinterpret_cast<float*>(parts);
+    a.part_ml = reinterpret_cast<float2*>(parts + round256((size_t)a.splits * rows_of(p) * p->D * sizeof(float)));
   }
   cudaStream_t st = (cudaStream_t)stream;
   const bool is_bf16 = p->dtype == BSA_BF16;
-  cudaError_t e;
+  cudaError_t e = cudaSuccess;
+  if (p->gathers && key_mask && (e = gather_keys(p, static_cast<char*>(ws), &a, st)) != cudaSuccess) return cuda_fail(e);
   if (is_bf16) {
     bsa::CrossMaps maps;
     bsa::CrossTiles t = p->fwd;
@@ -348,13 +386,16 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
     return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no query or gradient that repeats its heads (head stride 0)");
   const bool is_bf16 = p->dtype == BSA_BF16;
   a.lse = const_cast<float*>(lse);
-  a.delta = a.stats = static_cast<float*>(ws);
-  a.part_o = a.part_kv = reinterpret_cast<float*>(static_cast<char*>(ws) + stats_bytes(p));
+  char* sums = static_cast<char*>(ws) + gather_bytes(p);
+  a.delta = a.stats = reinterpret_cast<float*>(sums);
+  a.part_o = a.part_kv = reinterpret_cast<float*>(sums + stats_bytes(p));
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+  if (p->gathers && key_mask && (e = gather_keys(p, static_cast<char*>(ws), &a, st)) != cudaSuccess) return cuda_fail(e);
   bsa::CrossMaps maps;
   bsa::CrossTiles t = p->bwd;
   if (is_bf16 && (s = make_maps(p, a, true, &maps, &t)) != BSA_OK) return s;
-  cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = is_bf16 ? bsa::launch_cross_stats(a, t, p->D, st) : bsa::launch_cross_delta(a, p->D, st);
+  e = is_bf16 ? bsa::launch_cross_stats(a, t, p->D, st) : bsa::launch_cross_delta(a, p->D, st);
   a.splits = p->dq_splits;
   a.split_len = p->dq_len;
   if (e == cudaSuccess)
@@ -364,7 +405,7 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
   a.split_len = p->dkv_len;
   if (e == cudaSuccess)
     e = is_bf16 ? bsa::launch_cross_tc_dkv(a, t, maps, p->D, st) : bsa::launch_cross_f32_dkv(a, p->D, st);
-  if (e == cudaSuccess && a.splits > 1) e = bsa::launch_cross_reduce_kv(a, p->D, is_bf16, st);
+  if (e == cudaSuccess && (a.splits > 1 || a.slot_of)) e = bsa::launch_cross_reduce_kv(a, p->D, is_bf16, st);
   return e == cudaSuccess ? BSA_OK : cuda_fail(e);
 }
 

@@ -22,6 +22,49 @@ __device__ __forceinline__ void row_of(const CrossArgs& a, long long at, int& b,
   h = (int)(bh - (long long)b * a.heads);
 }
 
+// One CTA per batch element: the attended keys numbered in order.
+__global__ void __launch_bounds__(1024) cross_number_keys(CrossArgs a, int32_t* counts) {
+  __shared__ int s_warp[32];
+  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int keys = cross_keys(a, b);
+  const long long row = (long long)b * a.n_kv;
+  int before = 0;
+  for (int j0 = 0; j0 < a.n_kv; j0 += 1024) {
+    const int j = j0 + threadIdx.x;
+    const bool in = j < keys && __ldg(a.key_mask + row + j) != 0;
+    const uint32_t bits = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) s_warp[warp] = __popc(bits);
+    __syncthreads();
+    int lower = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      lower += w < warp ? s_warp[w] : 0;
+      all += s_warp[w];
+    }
+    if (j < a.n_kv) a.slot_of[row + j] = in ? before + lower + __popc(bits & ((1u << lane) - 1u)) : -1;
+    before += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) counts[b] = before;
+}
+
+// Copies the attended keys' rows of K (blockIdx.y 0) and V (1) to [B, n_kv,
+// heads_kv, D] without gaps, 16 bytes a thread; what lies behind a batch element's
+// count stays as it is.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_gather(CrossArgs a, T* k, T* v) {
+  constexpr int kPer = D * (int)sizeof(T) / 16, kEach = 16 / (int)sizeof(T);
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x, row = id / kPer;
+  if (row >= (long long)a.B * a.n_kv * a.heads_kv) return;
+  const int c = (int)(id % kPer) * kEach, hk = (int)(row % a.heads_kv);
+  const long long bj = row / a.heads_kv;
+  const int b = (int)(bj / a.n_kv), j = (int)(bj - (long long)b * a.n_kv), s = __ldg(a.slot_of + bj);
+  if (s < 0) return;
+  const View& from = blockIdx.y ? a.v : a.k;
+  T* to = (blockIdx.y ? v : k) + (((long long)b * a.n_kv + s) * a.heads_kv + hk) * D + c;
+  *reinterpret_cast<uint4*>(to) =
+      __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(from.p) + b * from.b + j * from.n + hk * from.h + c));
+}
+
 // One warp per row.  With partials (O_s, m_s, l_s) of the key splits:
 // M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s, and
 // lse = ln 2 (M + log2 sum w_s l_s).  A lane forms the weight of one split of 32,
@@ -126,20 +169,23 @@ __global__ void __launch_bounds__(256) cross_sum_q(CrossArgs a) {
   out4(reinterpret_cast<T*>(a.dq.p) + b * a.dq.b + n * a.dq.n + h * a.dq.h + c, acc);
 }
 
-// dK and dV from the partials of the row splits, added in order.
+// dK and dV from the partials of the row splits, added in order (of gathered keys:
+// from their places; the others get zeros).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_reduce_kv(CrossArgs a) {
   const long long all = (long long)a.B * a.heads_kv * a.n_kv;
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x, at = id / (D / 4);
   if (at >= all) return;
   const int c = (int)(id % (D / 4)) * 4, which = blockIdx.y;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.splits; ++s) {
-    const float4 x = in4(a.part_kv + ((2ll * s + which) * all + at) * D + c);
-    acc = make_float4(acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w);
-  }
   const long long bh = at / a.n_kv;
   const int j = (int)(at - bh * a.n_kv), b = (int)(bh / a.heads_kv), hk = (int)(bh % a.heads_kv);
+  const int place = a.slot_of ? __ldg(a.slot_of + (long long)b * a.n_kv + j) : j;
+  const long long from = bh * a.n_kv + place;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < (place < 0 ? 0 : a.splits); ++s) {
+    const float4 x = in4(a.part_kv + ((2ll * s + which) * all + from) * D + c);
+    acc = make_float4(acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w);
+  }
   const View& v = which ? a.dv : a.dk;
   out4(reinterpret_cast<T*>(v.p) + b * v.b + j * v.n + hk * v.h + c, acc);
 }
@@ -161,6 +207,23 @@ cudaError_t run_aux(int which, const CrossArgs& a, int D, bool is_bf16, cudaStre
 
 }  // namespace
 
+cudaError_t launch_cross_gather(const CrossArgs& a, int32_t* counts, void* k, void* v, int D, bool is_bf16,
+                                cudaStream_t st) {
+  cross_number_keys<<<a.B, 1024, 0, st>>>(a, counts);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long parts = (long long)a.B * a.n_kv * a.heads_kv * (D * (is_bf16 ? 2 : 4) / 16);
+  const dim3 grid((unsigned)((parts + 255) / 256), 2);
+  if (is_bf16) {
+    __nv_bfloat16 *k2 = static_cast<__nv_bfloat16*>(k), *v2 = static_cast<__nv_bfloat16*>(v);
+    if (D == 128) cross_gather<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(a, k2, v2);
+    else cross_gather<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(a, k2, v2);
+  } else {
+    if (D == 128) cross_gather<float, 128><<<grid, 256, 0, st>>>(a, static_cast<float*>(k), static_cast<float*>(v));
+    else cross_gather<float, 64><<<grid, 256, 0, st>>>(a, static_cast<float*>(k), static_cast<float*>(v));
+  }
+  return cudaGetLastError();
+}
 cudaError_t launch_cross_merge(const CrossArgs& a, int D, bool is_bf16, cudaStream_t st) {
   return run_aux(0, a, D, is_bf16, st);
 }

@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_f32_dkv(CrossArgs a) {
   for (int h = 0; h < 2; ++h) {
     const int j = j0 + 16 * warp + 8 * h + (lane >> 2);
     if (j >= a.n_kv) continue;
-    if (a.splits > 1) {
+    if (a.splits > 1 || a.slot_of) {
       const long long all = (long long)a.B * a.heads_kv * a.n_kv;
       const long long at = ((long long)b * a.heads_kv + hk) * a.n_kv + j;
       put_row<D>(a.part_kv + ((2ll * blockIdx.y) * all + at) * D, dk, h, lane, a.scale);

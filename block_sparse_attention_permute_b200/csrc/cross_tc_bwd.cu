@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j < a.n_kv) {
             const float by = which ? 1.0f : a.scale;
-            if (a.splits > 1)
+            if (a.splits > 1 || a.slot_of)
               store32(a.part_kv + ((2ll * split + which) * all + at) * HD + c0, o, by);
             else
               store32(reinterpret_cast<__nv_bfloat16*>(v.p) + b * v.b + j * v.n + hk * v.h + c0, o, by);

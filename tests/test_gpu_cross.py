@@ -148,6 +148,11 @@ SHAPES = [
     (2, 2, 150, 96, 1, 128, "length"),
     (3, 1, 1, 2, 1, 128, "none"),
     (1, 3000, 129, 1, 1, 64, "empty"),
+    (2, 2100, 300, 2, 2, 128, "holes"),
+    (2, 1050, 513, 4, 2, 64, "both"),
+    (2, 2048, 1500, 1, 1, 128, "empty"),
+    (2, 2048, 200, 3, 3, 64, "one"),
+    (1, 512, 2300, 8, 2, 128, "holes"),
 ]
 IDS = ["x".join(map(str, s)) for s in SHAPES]
 
@@ -176,7 +181,7 @@ def test_forward_and_gradients(shape, dtype, dev):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("n_q", [1, 150])
+@pytest.mark.parametrize("n_q", [1, 150, 1100])
 def test_masked_keys_may_hold_anything(n_q, dtype, dev):
     B, n_kv, H, hkv, D = 2, 200, 4, 2, 64
     op = bsa.CrossAttention(B, n_q, n_kv, H, hkv, D, dtype, device=dev)
@@ -334,7 +339,7 @@ def test_lengths_out_of_range_are_clamped_and_reported(dev):
 
 def test_writes_only_its_buffers(dev):
     for dtype in (torch.float32, torch.bfloat16):
-        for shape in ((1, 130, 70, 2, 1, 64), (2, 1, 900, 4, 2, 128)):
+        for shape in ((1, 130, 70, 2, 1, 64), (2, 1, 900, 4, 2, 128), (1, 2050, 140, 1, 1, 64)):
             B, n_q, n_kv, H, hkv, D = shape
             op = bsa.CrossAttention(*shape, dtype, device=dev)
             q, d_o = rand((B, n_q, H, D), dtype, dev, 1), rand((B, n_q, H, D), dtype, dev, 4)
@@ -347,14 +352,15 @@ def test_writes_only_its_buffers(dev):
 
             bufs = [guarded(s, dtype) for s in (q.shape, q.shape, k.shape, v.shape)]
             ws = [guarded((max(n, 256),), torch.uint8) for n in (op.forward_ws, op.backward_ws)]
-            _, lse = op.forward(q, k, v, out=bufs[0][1], return_lse=True, workspace=ws[0][1])
-            op.backward(d_o, q, k, v, bufs[0][1], lse, out=tuple(b[1] for b in bufs[1:]), workspace=ws[1][1])
+            m = masks("holes", B, n_kv, dev)
+            _, lse = op.forward(q, k, v, out=bufs[0][1], return_lse=True, workspace=ws[0][1], **m)
+            op.backward(d_o, q, k, v, bufs[0][1], lse, out=tuple(b[1] for b in bufs[1:]), workspace=ws[1][1], **m)
             op.check_status()
             for raw, body in bufs + ws:
                 n = body.numel() * body.element_size()
                 assert bool((raw[:4096] == 0xA5).all()) and bool((raw[4096 + n:] == 0xA5).all())
-            o, lse = op.forward(q, k, v, return_lse=True)
-            for x, y in zip((o, *op.backward(d_o, q, k, v, o, lse)), (b[1] for b in bufs)):
+            o, lse = op.forward(q, k, v, return_lse=True, **m)
+            for x, y in zip((o, *op.backward(d_o, q, k, v, o, lse, **m)), (b[1] for b in bufs)):
                 assert torch.equal(x, y)
 
 
