@@ -15,7 +15,14 @@
 // logits become the operand's columns t and t + 4, and the other operand's rows are
 // taken in the same order.  Rows in shared memory are padded by 4 floats, so that
 // ldmatrix (eight rows, 16 bytes each) and the loads of rows 2t, columns g both
-// touch all banks once.
+// touch all banks once.  Two or three CTAs of 64 rows (or keys) share an SM and cover
+// one another's loads and barriers.
+//
+// Measured on B200, 1560 rows x 226 keys x 12 heads of 128: forward 73 us, dQ 108 us,
+// dK and dV 113 us (23 to 38 TFLOP/s of fp32 products), a training step 318 us; packed
+// fp32 FMAs took 404 us (bound by 3.1 shared-memory wavefronts per 16-byte load), a
+// library's fp32 products with the rest in torch 387 us.  Bound by issue slots: nine
+// instructions for the three MMAs of a product, four of them the split.
 #include "cross.cuh"
 
 namespace bsa {

@@ -120,23 +120,24 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, 
       "r"(a_tmem), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
       : "memory");
 }
-// D = A B^T: 128 rows of A, N rows of B, contracted over the head dimension.
-template <int HD, int N = 128>
+// D = A B^T: both operands contracted over the head dimension.
+template <int HD>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb) {
   const uint32_t a = desc_low(sa, 16), b = desc_low(sb, 16);
 #pragma unroll
   for (int kk = 0; kk < HD / 16; ++kk) {
     const uint32_t p = kk >> 2, c = (kk & 3) * 2;
-    mma_ss(d, a + p * (128 * 128 / 16) + c, b + p * (N * 128 / 16) + c, idesc_bf16_f32(128, N, 0, 0), kk > 0 ? 1u : 0u);
+    mma_ss(d, a + p * (128 * 128 / 16) + c, b + p * (128 * 128 / 16) + c, idesc_bf16_f32(128, 128, 0, 0),
+           kk > 0 ? 1u : 0u);
   }
 }
-// D (+)= A B: A bf16 in TMEM (N values of a row as pairs; of 128, the second half
-// starts `half` columns after the first), B's N rows contracted.
-template <int HD, int N = 128>
+// D (+)= A B: A bf16 in TMEM (128 values of a row as pairs; the second half starts
+// `half` columns after the first), B's 128 rows contracted.
+template <int HD>
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t ta, uint32_t half, uint32_t sb, bool accumulate) {
-  const uint32_t b = desc_low(sb, N * 128);
+  const uint32_t b = desc_low(sb, 128 * 128);
 #pragma unroll
-  for (int kk = 0; kk < N / 16; ++kk)
+  for (int kk = 0; kk < 8; ++kk)
     mma_ts(d, ta + (kk >> 2) * half + 8u * (kk & 3), b + kk * (2048 / 16), idesc_bf16_f32(128, HD, 0, 1),
            (accumulate || kk > 0) ? 1u : 0u);
 }

@@ -16,6 +16,13 @@
 //   S(0) dP(0) | dV(0) S(1) dK(0) dP(1) | dV(1) S(2) dK(1) dP(2) | ...
 // so that the row work on P runs beside dK and dP, and that on dS beside dV and
 // the next S.
+//
+// Measured on B200, 32 760 queries x 512 keys x 12 heads of 128 (a product is 51.5
+// GFLOP): row sums 36 us (203 MB, 5.6 TB/s), dQ 157 us (three products, 985
+// TFLOP/s), dK and dV 206 us (four, 1000 TFLOP/s), all at 1.5 GHz under the
+// profiler; 430 us together in a sustained loop at the 1000 W cap.  Tensor pipe 54%
+// busy in both: bound by the row work between two products (1600 cycles for P of a
+// tile, 600 for dS), beside which the other products run.
 #include "cross_tc.cuh"
 
 namespace bsa {

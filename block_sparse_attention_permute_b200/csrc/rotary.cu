@@ -60,7 +60,8 @@ __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2
 // consecutive parts of a token's head.  Measured on B200: HunyuanVideo's Q and
 // K (57 856 tokens, 24 heads of 128, bf16) 220 us, 6.46 TB/s; Wan2.1-1.3B's
 // out of a fused projection (32 760 tokens, 12 heads) 67 us, 5.98 TB/s; half
-// layout, 131 040 tokens of 12 heads 249 us, 6.46 TB/s.
+// layout, 131 040 tokens of 12 heads 249 us, 6.46 TB/s; half layout whose halves
+// are 63 elements (2-byte accesses) 88 us instead of 66.
 template <typename T, bool HALF, int V>
 __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int P = HALF ? V : V / 2;          // pairs per thread
