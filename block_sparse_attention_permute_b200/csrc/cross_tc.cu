@@ -33,7 +33,6 @@
 namespace bsa {
 namespace {
 
-using Regs = RegSplit<208, 88>;
 constexpr float kRescale = 8.0f;   // log2 units by which a row's maximum may lag
 constexpr int kStep = 128;         // keys of a step
 
@@ -114,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kTmemSlot);
 
   if (warp >= 8) {
-    Regs::small();
+    give_up_registers();
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------------------ loads
       int pos[2] = {0, 0}, nq[2] = {0, 0};
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    Regs::rows();
+    take_row_registers();
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;    // stream, query row of the tile (TMEM lane)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128u * x + lane_off, tO = tmem + 256u + 128u * x + lane_off;

@@ -7,14 +7,16 @@ namespace bsa {
 
 constexpr int kThreads = 384;   // two warpgroups of row work, one of loads (warp 8) and MMAs (warp 9)
 // Registers: the launch gives kRegsLaunch to each thread; the load/MMA
-// warpgroup then drops to SMALL and the warpgroups of row work rise to ROWS.
-constexpr int kRegsLaunch = 168;
-template <int ROWS, int SMALL>
-struct RegSplit {
-  static_assert(2 * 128 * ROWS + 128 * SMALL <= kThreads * kRegsLaunch, "register split exceeds the launch");
-  static __device__ __forceinline__ void rows() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROWS)); }
-  static __device__ __forceinline__ void small() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SMALL)); }
-};
+// warpgroup then drops to kRegsSmall and the warpgroups of row work rise to
+// kRegsRows.  (216 and 72 spill in the MMA warp, 1 to 2% slower.)
+constexpr int kRegsLaunch = 168, kRegsRows = 200, kRegsSmall = 104;
+static_assert(2 * 128 * kRegsRows + 128 * kRegsSmall <= kThreads * kRegsLaunch, "register split exceeds the launch");
+__device__ __forceinline__ void take_row_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
+}
+__device__ __forceinline__ void give_up_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSmall));
+}
 
 // An item of the schedule: a K/V head of a batch element, a run of key steps, a
 // pair of query tiles (or one).

@@ -28,8 +28,6 @@
 namespace bsa {
 namespace {
 
-using DqRegs = RegSplit<200, 104>;
-using DkvRegs = RegSplit<216, 72>;
 
 // Shared memory of cross_tc_dq.
 template <int HD>
@@ -117,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kTmemSlot);
 
   if (warp >= 8) {
-    DqRegs::small();
+    give_up_registers();
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------------------ loads
       int g = 0, kv = 0, nq[2] = {0, 0}, no[2] = {0, 0};   // steps, K/V copies, copies of each Q and dO buffer
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ rows
-    DqRegs::rows();
+    take_row_registers();
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128u * x + lane_off, tQ = tmem + 256u + 128u * x + lane_off;
@@ -457,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS = tmem, tD = tmem + 128, tV = tmem + 256, tK = tmem + 384;
 
   if (warp >= 8) {
-    DkvRegs::small();
+    give_up_registers();
     if (warp == 8 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ loads
       mbar_arrive_expect_tx(bar(L::kKv), 2 * L::kTile);
@@ -536,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ keys
-    DkvRegs::rows();
+    take_row_registers();
     const int x = warp >> 2, r = (warp & 3) * 32 + lane, j = j0 + r;   // half of the queries, key
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     bool seen = j < keys;
@@ -549,10 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int i = 0; i < n; ++i) {
       const int st = i % L::kStages;
-      // -lse and -delta of the thread's 64 queries (the wait is for their copy)
+      // -lse and -delta of the thread's 64 queries (the wait is for their copy).
+      // -lse is read ahead of S: beside the MMAs' operands shared memory is slow
+      // (350 cycles of the step).
+      if (!(ok = wait(L::kQFull + st, i / L::kStages))) break;
       const float4* nl = reinterpret_cast<const float4*>(sm + L::kStat + st * 1024) + 16 * x;
       const float4* nd = nl + 32;
-      if (!(ok = wait(L::kQFull + st, i / L::kStages) && wait(L::kS, i))) break;
+      float4 lse[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) lse[c] = nl[c];
+      if (!(ok = wait(L::kS, i))) break;
       tc_fence_after();
       uint32_t p[64], pk[32];
       TMEM_LD32(tS + lane_off + 64 * x, (p + 0));
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       TMEM_LD_WAIT((p + 32));
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const float4 l = nl[c];
+        const float4 l = lse[c];
         const float2 e0 = fma2(make_float2(__uint_as_float(p[4 * c]), __uint_as_float(p[4 * c + 1])), sl2,
                                make_float2(l.x, l.y));
         const float2 e1 = fma2(make_float2(__uint_as_float(p[4 * c + 2]), __uint_as_float(p[4 * c + 3])), sl2,
