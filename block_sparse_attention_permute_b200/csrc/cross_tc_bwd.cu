@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!wait(L::kDp + x, g)) { ok = false; break; }
         tc_fence_after();
-        if (w.n == 1 && a.splits == 1) {
+        if (w.keys <= 128) {
           // All keys are here, so delta is the sum of P dP in fp32, not that of dO
           // with the rounded O: with few keys dP - delta cancels, and the rounding
           // of O was the largest error of dQ and dK (0.6% with two keys, else 0.25).

@@ -240,15 +240,17 @@ def test_shared_states_of_a_broadcast_batch(dev):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("kind", ["none", "length", "one"])
+@pytest.mark.parametrize("kind", ["none", "length", "one", "few queries", "many queries"])
 def test_one_key_has_no_gradient_of_its_logit(kind, dtype, dev):
     # softmax over one key is 1 whatever its logit: O = V, dQ = dK = 0 exactly
-    B, n_q, n_kv, H, D = 2, 130, 1 if kind == "none" else 40, 2, 64
+    # (few queries: the keys are split over CTAs; many: the attended keys are gathered)
+    B, H, D = 2, 2, 64
+    n_q, n_kv = {"few queries": (2, 5000), "many queries": (2100, 300), "none": (130, 1)}.get(kind, (130, 40))
     op = bsa.CrossAttention(B, n_q, n_kv, H, H, D, dtype, device=dev)
     q, d_o = rand((B, n_q, H, D), dtype, dev, 1, 3.0), rand((B, n_q, H, D), dtype, dev, 4)
     k, v = rand((B, n_kv, H, D), dtype, dev, 2), rand((B, n_kv, H, D), dtype, dev, 3)
-    m = {"kv_len": torch.ones(B, dtype=torch.int32, device=dev)} if kind == "length" else \
-        masks(kind, B, n_kv, dev) if kind == "one" else {}
+    m = {"kv_len": torch.ones(B, dtype=torch.int32, device=dev)} if kind in ("length", "few queries") else \
+        masks("one", B, n_kv, dev) if kind in ("one", "many queries") else {}
     o, lse = op.forward(q, k, v, return_lse=True, **m)
     ref = oracle(q, k, v, d_o, **m)
     check("o", o, ref["o"])
@@ -324,6 +326,55 @@ def test_captured_in_a_graph(dev):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
         for x, y in zip(g, op.backward(d_o, q, k, v, o2, lse2, kv_len=n)):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_gathered_keys_in_a_graph_with_another_mask(dtype, dev):
+    B, n_q, n_kv, H, D = 2, 2050, 260, 1, 64
+    op = bsa.CrossAttention(B, n_q, n_kv, H, H, D, dtype, device=dev)
+    x = [rand(s, dtype, dev, i) for i, s in enumerate((op.q_shape, op.kv_shape, op.kv_shape, op.q_shape))]
+    m = masks("holes", B, n_kv, dev)
+    o, lse = op.forward(*x[:3], return_lse=True, **m)
+    op.backward(x[3], *x[:3], o, lse, **m)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = op.forward(*x[:3], return_lse=True, **m)
+        g = op.backward(x[3], *x[:3], o, lse, **m)
+    for key_mask in (masks("holes", B, n_kv, dev, 9)["key_mask"], masks("empty", B, n_kv, dev, 3)["key_mask"],
+                     torch.ones((B, n_kv), dtype=torch.bool, device=dev)):
+        m["key_mask"].copy_(key_mask)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = oracle(*x, **m)
+        for name, t in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *g)):
+            check(name, t, ref[name])
+
+
+def test_nan_in_an_attended_key_shows(dev):
+    for dtype in (torch.float32, torch.bfloat16):
+        op = bsa.CrossAttention(1, 140, 200, 1, 1, 64, dtype, device=dev)
+        q, k, v = (rand(s, dtype, dev, i) for i, s in enumerate((op.q_shape, op.kv_shape, op.kv_shape)))
+        k[0, 150, 0, 3] = math.nan
+        assert torch.isnan(op.forward(q, k, v)).all()
+
+
+def test_offsets_past_32_bits(dev):
+    # K and V of 2.5e9 elements, one query token: the last keys count as much as the first
+    n_kv, H, D = 600_000, 32, 128
+    op = bsa.CrossAttention(1, 1, n_kv, H, H, D, torch.bfloat16, device=dev)
+    kv = [torch.empty((1, n_kv, H, D), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    g = torch.Generator(device=dev).manual_seed(1)
+    for t in kv:
+        for i in range(0, n_kv, 50_000):
+            t[:, i:i + 50_000].copy_(torch.randn((1, 50_000, H, D), generator=g, device=dev))
+    q = rand((1, 1, H, D), torch.bfloat16, dev, 2, 3.0)
+    o, lse = op.forward(q, *kv, return_lse=True)
+    op.check_status()
+    for h in (0, 17, 31):
+        ref = oracle(q[:, :, h:h + 1], kv[0][:, :, h:h + 1], kv[1][:, :, h:h + 1])
+        check("o", o[:, :, h:h + 1], ref["o"])
+        check("lse", lse[:, h:h + 1], ref["lse"])
 
 
 def test_lengths_out_of_range_are_clamped_and_reported(dev):

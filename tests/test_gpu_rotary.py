@@ -199,6 +199,24 @@ def test_captured_in_a_graph_reads_new_inputs(dev):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_offsets_past_32_bits(dev):
+    # 500 000 tokens of 40 heads of 128: the last token turns like one of a small grid at its place
+    grid, heads, D = (100, 50, 100), 40, 128
+    plan = bsa.Plan(1, *grid, 4, 4, 8, heads, D, 0, torch.bfloat16, dev)
+    rope = plan.rope((44, 42, 42))
+    q = torch.empty((1, 500_000, heads, D), dtype=torch.bfloat16, device=dev)
+    q[0, :499_000].fill_(1.0)
+    q[0, 499_000:].copy_(rand((1000, heads, D), torch.bfloat16, dev, 3))
+    tail = q[:, -100:].clone()
+    rope.apply(q, out=q)
+    small = bsa.Plan(1, 1, 50, 100, 4, 4, 8, heads, D, 0, torch.bfloat16, dev)
+    x = torch.zeros((1, 5000, heads, D), dtype=torch.bfloat16, device=dev)
+    x[:, -100:] = tail
+    want = small.rope((44, 42, 42)).apply(x, t_origin=torch.tensor([99], device=dev))
+    assert torch.equal(q[:, -100:], want[:, -100:])
+    del q
+
+
 def test_refusals(dev):
     plan = bsa.Plan(1, 2, 2, 2, 1, 1, 1, 2, 64, 0, torch.bfloat16, dev)
     rope = plan.rope((16, 24, 24))
