@@ -619,9 +619,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(L::kFinal, 0);
       tc_fence_after();
     }
-    // Stream x writes half of the columns of dV and dK; a key that is not
-    // attended gets zeros.
-    if (ok) {
+    // Stream x writes half of the columns of dV and dK (head dimension 64: one of
+    // the two); a key that is not attended gets zeros.
+    if (ok && n > 0 && a.splits == 1 && a.slot_of == nullptr) {
+      // through the places of K and V, which nothing reads any more, in runs of 128
+      // bytes (with few query rows this is most of a CTA's time)
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (HD == 64 && which != x) continue;
+        const int c0 = HD == 64 ? 0 : 64 * x;
+        uint32_t o[64];
+        TMEM_LD32((which ? tV : tK) + lane_off + c0, (o + 0));
+        TMEM_LD32((which ? tV : tK) + lane_off + c0 + 32, (o + 32));
+        TMEM_LD_WAIT((o + 0));
+        TMEM_LD_WAIT((o + 32));
+        if (!seen) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) o[c] = 0u;
+        }
+        uint8_t* stage = sm + (which ? L::kV : L::kK) + (HD == 64 ? warp & 3 : warp) * 4096;
+        stage_rows64(stage, o, which ? 1.0f : a.scale, lane);
+        __syncwarp();
+        const View& v = which ? a.dv : a.dk;
+        __nv_bfloat16* base =
+            reinterpret_cast<__nv_bfloat16*>(v.p) + b * v.b + hk * v.h + c0 + (lane & 7) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = 4 * i + (lane >> 3), key = j0 + (warp & 3) * 32 + k;
+          if (key < a.n_kv)
+            *reinterpret_cast<uint4*>(base + key * v.n) =
+                *reinterpret_cast<const uint4*>(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+        }
+      }
+    } else if (ok) {
       const long long all = (long long)a.B * a.heads_kv * a.n_kv, at = (long long)bh * a.n_kv + j;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
