@@ -679,7 +679,11 @@ class CrossAttention:
         return (None if kv_len is None else kv_len.data_ptr(),
                 None if key_mask is None else key_mask.data_ptr())
 
-    def _workspace(self, ws, need):
+    def _workspace(self, ws, need, dev_status):
+        for t, types, name in ((ws, None, "workspace"), (dev_status, torch.int32, "dev_status")):
+            if t is not None and (not isinstance(t, torch.Tensor) or t.device != self.device or
+                                  not t.is_contiguous() or (types and (t.dtype != types or not t.numel()))):
+                raise BsaError(1, f"{name} must be a contiguous {f'{types} ' if types else ''}tensor on {self.device}")
         if ws is None and need:
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size()), ws
@@ -704,7 +708,7 @@ class CrossAttention:
         lse = torch.empty(self.lse_shape, dtype=torch.float32, device=self.device) if return_lse else None
         keep, views = _views(q, k, v, out)
         masks = self._masks(kv_len, key_mask)
-        ws, keep_ws = self._workspace(workspace, self.forward_ws)
+        ws, keep_ws = self._workspace(workspace, self.forward_ws, dev_status)
         _call(self.device, load().bsa_cross_attention, self._h, *views[:3], *masks, views[3],
               None if lse is None else lse.data_ptr(), *ws,
               None if dev_status is None else dev_status.data_ptr())
@@ -726,7 +730,7 @@ class CrossAttention:
         dq, dk, dv = out
         keep, views = _views(q, k, v, o, d_o, dq, dk, dv)
         masks = self._masks(kv_len, key_mask)
-        ws, keep_ws = self._workspace(workspace, self.backward_ws)
+        ws, keep_ws = self._workspace(workspace, self.backward_ws, dev_status)
         _call(self.device, load().bsa_cross_attention_backward, self._h, *views[:3], *masks, views[3],
               lse.data_ptr(), *views[4:], *ws, None if dev_status is None else dev_status.data_ptr())
         return dq, dk, dv

@@ -338,6 +338,8 @@ bsa_status bsa_cross_attention(bsa_cross_t p, const bsa_view_t* q, const bsa_vie
   bsa::CrossArgs a;
   if ((s = fill(p, q, k, v, o, true, kv_len, key_mask, dev_status, &a)) != BSA_OK) return s;
   if ((s = check_ws(ws, ws_bytes, forward_bytes(p))) != BSA_OK) return s;
+  for (const bsa::View* in : {&a.q, &a.k, &a.v})
+    if (a.o.p == in->p) return fail(BSA_ERR_INVALID_ARG, "an output is the memory of an input");
   a.lse = lse;
   a.splits = p->fwd_splits;
   a.split_len = p->fwd_len;
@@ -379,6 +381,9 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
   if (lse == nullptr) return fail(BSA_ERR_INVALID_ARG, "lse is NULL");
   if (a.dq.p == a.dk.p || a.dq.p == a.dv.p || a.dk.p == a.dv.p)
     return fail(BSA_ERR_INVALID_ARG, "dq, dk and dv are the same memory");
+  for (const bsa::View* out : {&a.dq, &a.dk, &a.dv})
+    for (const bsa::View* in : {&a.q, &a.k, &a.v, &a.o, &a.d_o})
+      if (out->p == in->p) return fail(BSA_ERR_INVALID_ARG, "an output is the memory of an input");
   if ((s = check_ws(ws, ws_bytes, backward_bytes(p))) != BSA_OK) return s;
   if (p->n_q > 1 && a.d_o.n == 0)
     return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no view that repeats its tokens (token stride 0)");

@@ -537,6 +537,43 @@ def test_refusals(dev):
     torch.cuda.synchronize()
 
 
+def test_refuses_workspace_and_status_elsewhere(dev):
+    """Working memory and a status word that no kernel could write."""
+    op = bsa.CrossAttention(1, 4, 3000, 2, 1, 64, torch.bfloat16, device=dev)
+    q = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16, device=dev)
+    k = torch.zeros((1, 3000, 1, 64), dtype=torch.bfloat16, device=dev)
+    room = max(op.forward_ws, op.backward_ws, 256)
+    o, lse = op.forward(q, k, k, return_lse=True)
+    for bad in (torch.empty(room, dtype=torch.uint8), torch.empty(2 * room, dtype=torch.uint8, device=dev)[::2], room):
+        with pytest.raises(bsa.BsaError, match="workspace must be"):
+            op.forward(q, k, k, workspace=bad)
+        with pytest.raises(bsa.BsaError, match="workspace must be"):
+            op.backward(q, q, k, k, o, lse, workspace=bad)
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64, device=dev),
+                torch.zeros(0, dtype=torch.int32, device=dev)):
+        with pytest.raises(bsa.BsaError, match="dev_status must be"):
+            op.forward(q, k, k, dev_status=bad)
+        with pytest.raises(bsa.BsaError, match="dev_status must be"):
+            op.backward(q, q, k, k, o, lse, dev_status=bad)
+    torch.cuda.synchronize()
+
+
+def test_refuses_outputs_over_inputs(dev):
+    """Tiles of an output are written while others of the inputs are still to be read."""
+    op = bsa.CrossAttention(1, 300, 300, 2, 2, 64, torch.bfloat16, device=dev)
+    q, k, v, do = (torch.zeros((1, 300, 2, 64), dtype=torch.bfloat16, device=dev) for _ in range(4))
+    for out in (q, k, v):
+        with pytest.raises(bsa.BsaError, match="memory of an input"):
+            op.forward(q, k, v, out=out)
+    o, lse = op.forward(q, k, v, return_lse=True)
+    new = [torch.empty_like(q) for _ in range(3)]
+    for at in range(3):
+        for t in (q, k, v, o, do):
+            with pytest.raises(bsa.BsaError, match="memory of an input"):
+                op.backward(do, q, k, v, o, lse, out=tuple(t if i == at else x for i, x in enumerate(new)))
+    torch.cuda.synchronize()
+
+
 def test_rotary_self_attention_cross_attention_together(dev):
     """One block's attention path: rotate Q and K of a fused projection, block-sparse self-attention
     over the rotated tensors, cross attention of its output over text states, and the gradients back
