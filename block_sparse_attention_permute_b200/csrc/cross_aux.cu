@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(256) cross_gather(CrossArgs a, T* k, T* v) {
 
 // One warp per row.  With partials (O_s, m_s, l_s) of the key splits:
 // M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s, and
-// lse = ln 2 (M + log2 sum w_s l_s).  A lane forms the weight of one split of 32,
+// lse = ln 2 (M + log2 sum w_s l_s).  A split without attended keys is told by
+// l_s = 0, never by m_s = -inf: logits that are all NaN leave that maximum too, and
+// their l_s = NaN has to reach the result.  A lane forms the weight of one split of 32,
 // then takes its columns (D = 64: half a warp every other split) of them all.  Few
 // rows leave latency as the bound, so sixteen partial rows are in flight, asked for
 // before their weights are known: 5 us for 64 rows of 18 splits, 48 us with one row
@@ -84,6 +86,7 @@ __global__ void __launch_bounds__(128) cross_merge(CrossArgs a) {
   for (int s32 = 0; s32 < a.splits; s32 += 32) {
     const int mine = s32 + lane;
     const float2 ml = mine < a.splits ? __ldg(a.part_ml + mine * rows + at) : make_float2(-INFINITY, 0.f);
+    const uint32_t some = __ballot_sync(0xffffffffu, ml.y != 0.f);     // splits with attended keys
     float top = 0.f, w = 0.f;
     for (int s0 = s32; s0 < min(s32 + 32, a.splits); s0 += kFlight * kHalves) {
       float4 x[kFlight];
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(128) cross_merge(CrossArgs a) {
         top = fmaxf(top, M);
         const float base = top == -INFINITY ? 0.f : top, keep = exp2f(M - base);
         w = exp2f(ml.x - base);
-        float sum = ml.x == -INFINITY ? 0.f : w * ml.y;
+        float sum = ml.y == 0.f ? 0.f : w * ml.y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         l = fmaf(l, keep, sum);
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(128) cross_merge(CrossArgs a) {
       for (int u = 0; u < kFlight; ++u) {
         const int s = s0 + u * kHalves + first;
         const float ws = __shfl_sync(0xffffffffu, w, s & 31);
-        if (s < a.splits && ws != 0.f)      // a split without keys (m = -inf, w = 0) has not written its O
+        if ((some >> (s & 31)) & 1u)        // (a split without keys need not have written its O)
           acc = make_float4(fmaf(ws, x[u].x, acc.x), fmaf(ws, x[u].y, acc.y), fmaf(ws, x[u].z, acc.z),
                             fmaf(ws, x[u].w, acc.w));
       }
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(128) cross_merge(CrossArgs a) {
     acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
     acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   int b, h, n;
   row_of(a, at, b, h, n);
   if (first == 0)

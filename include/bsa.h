@@ -578,7 +578,8 @@ bsa_status bsa_rotary(bsa_rope_t rope, const bsa_view_t* q, const bsa_view_t* k,
  * element, from n_q query tokens to n_kv encoder states; head h of Q reads
  * head h / (heads / heads_kv) of K and V.  A key is attended if it is below
  * kv_len[b] and its key_mask byte is not 0; what K and V hold at the other
- * keys (also infinities and NaN) does not enter.  A batch element without
+ * keys (also infinities and NaN) does not enter; a NaN in a query or at an
+ * attended key makes the rows that it enters NaN.  A batch element without
  * attended keys gives O = 0, lse = -inf and zero gradients. */
 typedef struct bsa_cross_s* bsa_cross_t;
 
