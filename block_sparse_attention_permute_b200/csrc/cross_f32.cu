@@ -6,8 +6,9 @@
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
 // Products run on the tensor cores in tf32, three for one: with x = h + l, h the 11
 // leading bits that tf32 keeps, a b = ha hb + ha lb + la hb up to 2^-20 of its size
-// (la lb, and what tf32 drops of l), every sum in fp32; the small products of a
-// tile have a sum of their own, as the tensor core rounds each addition to zero.  The
+// (la lb, and what tf32 drops of l), every sum in fp32.  As the tensor core rounds
+// each addition toward zero, a tile's products are summed from zero, the small ones
+// apart from the large, and joined to the running sum by fp32 additions.  The
 // legacy warp MMA serves here: tcgen05 would want both parts of both operands in
 // shared memory, 256 KB for one pair of 128 x 128 tiles.  A warp owns 16 rows of
 // the result (query rows; keys for dK and dV) and keeps its logits, probabilities
@@ -149,7 +150,10 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int lan
 }
 
 // acc[n] += P (16 rows, 32 columns held as dot_tile leaves them) times the 32 rows
-// of B, columns 8 n .. 8 n + 7.
+// of B, columns 8 n .. 8 n + 7.  The tile's products start from zero and join acc
+// by an fp32 addition to nearest: carried from tile to tile in the MMA, whose
+// additions all round toward zero, a sum of terms of one sign lost 2.4e-4 of itself
+// over 32 768 rows.
 template <int D>
 __device__ __forceinline__ void sum_tile(const float (&p)[4][4], const float* B, int lane, float (&acc)[D / 8][4]) {
   const float* q = B + 2 * (lane & 3) * row_floats<D>() + (lane >> 2);
@@ -162,14 +166,14 @@ __device__ __forceinline__ void sum_tile(const float (&p)[4][4], const float* B,
   }
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) {
-    float small[4] = {0.f, 0.f, 0.f, 0.f};
+    float large[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float* b = q + 8 * j * row_floats<D>() + 8 * n;
-      mma3(acc[n], small, x[j], __float_as_uint(b[0]), __float_as_uint(b[row_floats<D>()]));
+      mma3(large, small, x[j], __float_as_uint(b[0]), __float_as_uint(b[row_floats<D>()]));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] += small[i];
+    for (int i = 0; i < 4; ++i) acc[n][i] += large[i] + small[i];
   }
 }
 
