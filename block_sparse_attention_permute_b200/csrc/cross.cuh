@@ -27,6 +27,7 @@ struct CrossArgs {
   // their counts, key_mask null): place of each key among them, -1 if none.  dK and
   // dV then always go through part_kv.
   int32_t* slot_of;          // [B, n_kv] or null
+  int32_t* attended;         // [B] attended keys, 2 for more (backward with a key mask) or null
   int B, n_q, n_kv, heads, heads_kv, group;
   int splits;                // of the kernel at hand
   int split_len;             // key tiles or steps (forward, dQ) or row tiles (dK, dV) per split
@@ -47,19 +48,28 @@ __device__ __forceinline__ int cross_keys(const CrossArgs& a, int b) {
   return c;
 }
 
-// Whether batch element b attends exactly one key (asked where they could all be in
-// one tile; whole warp).  Its P is 1 and its dS 0, exactly, which P from a rounded
-// lse would miss by an ulp.
+// Whether batch element b attends exactly one key.  Its P is 1 and its dS 0, exactly,
+// which P from a rounded lse and delta from a rounded O would miss by an ulp.
 __device__ __forceinline__ bool one_key(const CrossArgs& a, int b, int keys) {
-  if (keys > 128) return false;
+  return (a.attended ? __ldg(a.attended + b) : keys) == 1;
+}
+
+// attended[b] under the key mask, by a CTA of 256 threads: 4096 keys a time, until
+// there are two.
+__device__ __forceinline__ void count_keys(const CrossArgs& a, int b) {
+  const int keys = cross_keys(a, b);
+  const uint8_t* mask = a.key_mask + (long long)b * a.n_kv;
   int n = 0;
+  for (int j0 = 0; j0 < keys && n < 2; j0 += 4096) {
+    int mine = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = 32 * i + (threadIdx.x & 31);
-    n += __popc(__ballot_sync(0xffffffffu, j < keys && (a.key_mask == nullptr ||
-                                                        __ldg(a.key_mask + (long long)b * a.n_kv + j) != 0)));
+    for (int i = 0; i < 16; ++i) {
+      const int j = j0 + 256 * i + (int)threadIdx.x;
+      mine += j < keys && __ldg(mask + j) != 0;
+    }
+    n += __syncthreads_count(mine > 0) + __syncthreads_count(mine > 1);
   }
-  return n == 1;
+  if (threadIdx.x == 0) a.attended[b] = min(n, 2);
 }
 
 // Schedule of the tensor-core kernels.  A query tile is 128 rows: `tokens`

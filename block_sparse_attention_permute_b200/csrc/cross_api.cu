@@ -146,6 +146,8 @@ bsa_status make_map(CUtensorMap* m, const bsa::View& v, int B, int n, int heads,
 
 size_t rows_of(const bsa_cross_s* p) { return (size_t)p->B * p->heads * p->n_q; }
 
+size_t counts_bytes(const bsa_cross_s* p) { return round256((size_t)p->B * sizeof(int32_t)); }
+
 // Where a call's workspace begins when it gathers keys: their places, the counts,
 // the copies of K and V.
 size_t kv_copy_bytes(const bsa_cross_s* p) {
@@ -153,8 +155,7 @@ size_t kv_copy_bytes(const bsa_cross_s* p) {
 }
 size_t gather_bytes(const bsa_cross_s* p) {
   if (!p->gathers) return 0;
-  return round256((size_t)p->B * p->n_kv * sizeof(int32_t)) + round256((size_t)p->B * sizeof(int32_t)) +
-         2 * kv_copy_bytes(p);
+  return round256((size_t)p->B * p->n_kv * sizeof(int32_t)) + counts_bytes(p) + 2 * kv_copy_bytes(p);
 }
 
 size_t forward_bytes(const bsa_cross_s* p) {
@@ -166,8 +167,8 @@ size_t forward_bytes(const bsa_cross_s* p) {
 }
 
 // Backward workspace, after the gathered keys: the row sums (with lse in the query
-// tiles' order on the tensor cores), then the partials of dQ, whose place those of
-// dK and dV take.
+// tiles' order on the tensor cores), the counts of attended keys, then the partials
+// of dQ, whose place those of dK and dV take.
 size_t stats_bytes(const bsa_cross_s* p) {
   return p->dtype == BSA_BF16 ? round256((size_t)p->B * p->heads_kv * p->bwd.tiles * 256 * sizeof(float))
                               : round256(rows_of(p) * sizeof(float));
@@ -176,7 +177,7 @@ size_t backward_bytes(const bsa_cross_s* p) {
   const size_t q = p->dq_splits > 1 ? (size_t)p->dq_splits * rows_of(p) : 0;
   const size_t kv =
       p->dkv_splits > 1 || p->gathers ? (size_t)p->dkv_splits * 2 * p->B * p->heads_kv * p->n_kv : 0;
-  return gather_bytes(p) + stats_bytes(p) + round256((q > kv ? q : kv) * p->D * sizeof(float));
+  return gather_bytes(p) + stats_bytes(p) + counts_bytes(p) + round256((q > kv ? q : kv) * p->D * sizeof(float));
 }
 
 // Copies the attended rows of K and V together at the start of `ws` and lets *a
@@ -185,7 +186,7 @@ cudaError_t gather_keys(const bsa_cross_s* p, char* ws, bsa::CrossArgs* a, cudaS
   a->slot_of = reinterpret_cast<int32_t*>(ws);
   ws += round256((size_t)p->B * p->n_kv * sizeof(int32_t));
   int32_t* counts = reinterpret_cast<int32_t*>(ws);
-  ws += round256((size_t)p->B * sizeof(int32_t));
+  ws += counts_bytes(p);
   char *k = ws, *v = ws + kv_copy_bytes(p);
   const cudaError_t e = bsa::launch_cross_gather(*a, counts, k, v, p->D, p->dtype == BSA_BF16, st);
   const long long h = p->heads_kv > 1 ? p->D : 0, n = p->n_kv > 1 ? (long long)p->heads_kv * p->D : 0;
@@ -393,7 +394,8 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
   a.lse = const_cast<float*>(lse);
   char* sums = static_cast<char*>(ws) + gather_bytes(p);
   a.delta = a.stats = reinterpret_cast<float*>(sums);
-  a.part_o = a.part_kv = reinterpret_cast<float*>(sums + stats_bytes(p));
+  a.part_o = a.part_kv = reinterpret_cast<float*>(sums + stats_bytes(p) + counts_bytes(p));
+  if (key_mask && !p->gathers) a.attended = reinterpret_cast<int32_t*>(sums + stats_bytes(p));
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
   if (p->gathers && key_mask && (e = gather_keys(p, static_cast<char*>(ws), &a, st)) != cudaSuccess) return cuda_fail(e);

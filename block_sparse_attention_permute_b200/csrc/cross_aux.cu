@@ -135,10 +135,14 @@ __global__ void __launch_bounds__(128) cross_merge(CrossArgs a) {
 }
 
 // A group of D / 4 threads per (token, head) row; neighbouring groups take
-// neighbouring heads of a token.
+// neighbouring heads of a token.  (CTAs from `row_ctas` on count keys.)
 template <int D>
-__global__ void __launch_bounds__(256) cross_delta(CrossArgs a) {
+__global__ void __launch_bounds__(256) cross_delta(CrossArgs a, unsigned row_ctas) {
   constexpr int G = D / 4;
+  if (blockIdx.x >= row_ctas) {
+    count_keys(a, (int)(blockIdx.x - row_ctas));
+    return;
+  }
   const long long rows = cross_rows(a), id = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
   float sum = 0.f;
   int b = 0, h = 0, n = 0;
@@ -240,8 +244,9 @@ cudaError_t launch_cross_reduce_kv(const CrossArgs& a, int D, bool is_bf16, cuda
 }
 cudaError_t launch_cross_delta(const CrossArgs& a, int D, cudaStream_t st) {
   const unsigned ctas = (unsigned)((cross_rows(a) + 1024 / D - 1) / (1024 / D));
-  if (D == 128) cross_delta<128><<<ctas, 256, 0, st>>>(a);
-  else cross_delta<64><<<ctas, 256, 0, st>>>(a);
+  const unsigned more = a.attended ? (unsigned)a.B : 0u;
+  if (D == 128) cross_delta<128><<<ctas + more, 256, 0, st>>>(a, ctas);
+  else cross_delta<64><<<ctas + more, 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }
 

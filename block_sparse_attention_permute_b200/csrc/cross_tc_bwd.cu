@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nd = __ldg(a.stats + (long long)q.at * 256 + 128 + r);
       }
       const float2 nl2 = make_float2(nl, nl);
+      const bool one = one_key(a, w.b, w.keys);
       for (int s = 0; s < w.n; ++s, ++g) {
         const int j0 = (w.kt + s) * 128;
         const bool partial = a.key_mask != nullptr || j0 + 128 > w.keys;
@@ -330,10 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           nd = -(sum.x + sum.y);
           if (q.real) a.stats[(long long)q.at * 256 + 128 + r] = nd;     // for dK
-          if (one_key(a, w.b, w.keys)) {
+        }
+        if (one) {                        // dS = 0; a NaN stays one
 #pragma unroll
-            for (int c = 0; c < 128; ++c) p[c] = 0u;
-          }
+          for (int c = 0; c < 128; ++c) p[c] = __float_as_uint(__uint_as_float(p[c]) * 0.f);
         }
         const float2 nd2 = make_float2(nd, nd);
 #pragma unroll
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     bool seen = j < keys;
     if (seen && a.key_mask) seen = __ldg(a.key_mask + (long long)b * a.n_kv + j) != 0;
-    const bool one = one_key(a, b, keys), flat = !seen || one;      // dS of the key is 0
+    const bool one = one_key(a, b, keys);
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
     auto wait = [&](int y, int phase) {
@@ -585,6 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar(L::kP));
+      if (one) {                          // dS = 0; a NaN stays one
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] = __float_as_uint(__uint_as_float(p[c]) * 0.f);
+      }
       if (!(ok = wait(L::kDp, i))) break;
       tc_fence_after();
 #pragma unroll
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[16 * h + 2 * c + 1] = pack_bf16x2(v1.x, v1.y);
         }
       }
-      if (flat) {
+      if (!seen) {
 #pragma unroll
         for (int c = 0; c < 32; ++c) pk[c] = 0u;
       }
@@ -692,10 +697,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -lse in log2 units and -delta of every row of every query tile, in the
 // tiles' row order: HD / 8 threads per row, 16 bytes of O and dO each, four rows
 // per thread so that enough loads are in flight (one row: 49 us instead of 37 for
-// 200 MB).  Rows without a token, or without keys, get -inf and so P = 0.
+// 200 MB).  Rows without a token, or without keys, get -inf and so P = 0.  (CTAs from
+// `row_ctas` on count keys.)
 template <int HD>
 __global__ void __launch_bounds__(256) cross_stats(const __grid_constant__ CrossArgs a,
-                                                   const __grid_constant__ CrossTiles t) {
+                                                   const __grid_constant__ CrossTiles t, unsigned row_ctas) {
+  if (blockIdx.x >= row_ctas) {
+    count_keys(a, (int)(blockIdx.x - row_ctas));
+    return;
+  }
   constexpr int G = HD / 8, kRows = 4, kGroups = 256 / G;      // kGroups * kRows divides 128
   const long long first = (long long)blockIdx.x * kGroups * kRows;
   const long long tile = first >> 7;
@@ -770,8 +780,9 @@ cudaError_t prepare_cross_tc_backward(int D) { return D == 128 ? prepare<128>() 
 cudaError_t launch_cross_stats(const CrossArgs& a, const CrossTiles& t, int D, cudaStream_t st) {
   const long long rows = (long long)a.B * a.heads_kv * t.tiles * 128;
   const unsigned ctas = (unsigned)(rows * (D / 8) / (256 * 4));
-  if (D == 128) cross_stats<128><<<ctas, 256, 0, st>>>(a, t);
-  else cross_stats<64><<<ctas, 256, 0, st>>>(a, t);
+  const unsigned more = a.attended ? (unsigned)a.B : 0u;
+  if (D == 128) cross_stats<128><<<ctas + more, 256, 0, st>>>(a, t, ctas);
+  else cross_stats<64><<<ctas + more, 256, 0, st>>>(a, t, ctas);
   return cudaGetLastError();
 }
 

@@ -634,7 +634,10 @@ bsa_status bsa_cross_attention(bsa_cross_t cross, const bsa_view_t* q,
  * Every sum has a fixed order: two calls on the same inputs agree bit for
  * bit.  With bf16 and more than 128 keys the row sums of d_o * o are taken with
  * o as it is rounded, an error of about 0.2% of dq and dk in norm beside the
- * 0.25% of bf16 operands; with fewer keys they come from P and d_o V^T in fp32. */
+ * 0.25% of bf16 operands, and more where a key_mask leaves very few of them
+ * (0.6% with two); with fewer keys they come from P and d_o V^T in fp32.  (Keys
+ * are those below kv_len; with 2048 query rows or more to a K/V head those that
+ * the key_mask leaves.)  One attended key gives exact zeros in dq and dk. */
 bsa_status bsa_cross_attention_backward(
     bsa_cross_t cross, const bsa_view_t* q, const bsa_view_t* k,
     const bsa_view_t* v, const int32_t* kv_len, const uint8_t* key_mask,
