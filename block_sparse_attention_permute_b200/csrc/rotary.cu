@@ -295,6 +295,9 @@ bsa_status bsa_rotary(bsa_rope_t r, const bsa_view_t* q, const bsa_view_t* k, co
       return bsa_internal_fail(BSA_ERR_INVALID_ARG, "an output starts at its input but has other strides");
   }
   if (k && a.out[0].p == a.out[1].p) return bsa_internal_fail(BSA_ERR_INVALID_ARG, "q_out and k_out are the same memory");
+  // (threads turn a token's Q before its K, and CTAs in any order)
+  if (k && (a.out[0].p == a.in[1].p || a.out[1].p == a.in[0].p))
+    return bsa_internal_fail(BSA_ERR_INVALID_ARG, "q_out is the memory of k, or k_out that of q");
   a.rows = (long long)g.B * g.n_tot;
   a.n_video = g.n_video;
   a.div_tot = make_fastdiv((uint32_t)g.n_tot);
