@@ -216,8 +216,8 @@ bsa_status check_ws(const void* ws, size_t have, size_t need) {
 
 // The views and scalars that both directions take.
 bsa_status fill(const bsa_cross_s* p, const bsa_view_t* q, const bsa_view_t* k, const bsa_view_t* v,
-                const bsa_view_t* o, bool o_written, const int32_t* kv_len, const uint8_t* key_mask,
-                int32_t* dev_status, bsa::CrossArgs* a) {
+                const bsa_view_t* o, bool o_written, const float* lse, const int32_t* kv_len,
+                const uint8_t* key_mask, int32_t* dev_status, bsa::CrossArgs* a) {
   std::memset(a, 0, sizeof(*a));
   const int esz = p->dtype == BSA_BF16 ? 2 : 4;
   bsa_status s;
@@ -230,6 +230,9 @@ bsa_status fill(const bsa_cross_s* p, const bsa_view_t* q, const bsa_view_t* k, 
   if (p->heads > 1 && a->q.h == 0)
     return fail(BSA_ERR_UNSUPPORTED, "cross attention takes no query or gradient that repeats its heads (head stride 0)");
   if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return fail(BSA_ERR_INVALID_ARG, "kv_len must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(BSA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(dev_status) & 3u)
+    return fail(BSA_ERR_INVALID_ARG, "dev_status must be 4-byte aligned");
   a->kv_len = kv_len;
   a->key_mask = key_mask;
   a->B = p->B; a->n_q = p->n_q; a->n_kv = p->n_kv; a->heads = p->heads; a->heads_kv = p->heads_kv;
@@ -337,7 +340,7 @@ bsa_status bsa_cross_attention(bsa_cross_t p, const bsa_view_t* q, const bsa_vie
   bsa_status s = check_cross(p);
   if (s != BSA_OK) return s;
   bsa::CrossArgs a;
-  if ((s = fill(p, q, k, v, o, true, kv_len, key_mask, dev_status, &a)) != BSA_OK) return s;
+  if ((s = fill(p, q, k, v, o, true, lse, kv_len, key_mask, dev_status, &a)) != BSA_OK) return s;
   if ((s = check_ws(ws, ws_bytes, forward_bytes(p))) != BSA_OK) return s;
   for (const bsa::View* in : {&a.q, &a.k, &a.v})
     if (a.o.p == in->p) return fail(BSA_ERR_INVALID_ARG, "an output is the memory of an input");
@@ -373,7 +376,7 @@ bsa_status bsa_cross_attention_backward(bsa_cross_t p, const bsa_view_t* q, cons
   bsa_status s = check_cross(p);
   if (s != BSA_OK) return s;
   bsa::CrossArgs a;
-  if ((s = fill(p, q, k, v, o, false, kv_len, key_mask, dev_status, &a)) != BSA_OK) return s;
+  if ((s = fill(p, q, k, v, o, false, lse, kv_len, key_mask, dev_status, &a)) != BSA_OK) return s;
   const int esz = p->dtype == BSA_BF16 ? 2 : 4;
   if ((s = bsa::check_view(d_o, "d_o", p->B, p->n_q, p->heads, p->D, esz, false, &a.d_o)) != BSA_OK) return s;
   if ((s = bsa::check_view(dq, "dq", p->B, p->n_q, p->heads, p->D, esz, true, &a.dq)) != BSA_OK) return s;
