@@ -1,5 +1,6 @@
 // cross_api.cu — the C ABI of cross attention (bsa_cross_*): argument checks,
 // the split of each launch, workspace carving and launches.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -296,6 +297,8 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
   const double sc = scale > 0.0 ? scale : 1.0 / std::sqrt((double)head_dim);
   c.scale = (float)sc;
   c.scale_log2 = (float)(sc * 1.4426950408889634);
+  if (!(c.scale >= FLT_MIN) || !(c.scale_log2 <= FLT_MAX))
+    return fail(BSA_ERR_INVALID_ARG, "scale must be a normal number in fp32");
   if (dtype == BSA_BF16) plan_tc(&c);
   else plan_f32(&c);
   // Gathering costs two launches and one more pass over K and V; with 2048 query

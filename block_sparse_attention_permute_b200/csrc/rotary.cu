@@ -4,6 +4,7 @@
 // a sin w + b cos w) with w = pos f, pos the token's t, y or x and f the
 // pair's frequency.  The map is linear and its transpose turns by -w, so the
 // backward pass is the same kernel with the sine negated.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -210,8 +211,8 @@ bsa_status bsa_rope_create(bsa_rope_t* out, bsa_plan_t plan, const bsa_rope_conf
     return bsa_internal_fail(BSA_ERR_INVALID_ARG, "bad rope scaling");
   if (!(c->theta > 1.0) || !std::isfinite(c->theta))
     return bsa_internal_fail(BSA_ERR_INVALID_ARG, "rope theta must be above 1");
-  if (!(c->mscale > 0.0) || !std::isfinite(c->mscale))
-    return bsa_internal_fail(BSA_ERR_INVALID_ARG, "rope mscale must be above 0");
+  if (!(c->mscale >= FLT_MIN) || !(c->mscale <= FLT_MAX))
+    return bsa_internal_fail(BSA_ERR_INVALID_ARG, "rope mscale must be above 0 and a normal number in fp32");
   for (int x = 0; x < 3; ++x) {
     if (c->scaling != BSA_ROPE_NONE && (!(c->factor[x] >= 1.0) || !std::isfinite(c->factor[x])))
       return bsa_internal_fail(BSA_ERR_INVALID_ARG, "rope factor must be at least 1");

@@ -542,7 +542,8 @@ typedef struct {
   double factor[3];        /* >= 1 (read unless scaling is BSA_ROPE_NONE)     */
   double orig_len[3];      /* > 0 (BSA_ROPE_YARN)                             */
   double beta_fast, beta_slow; /* beta_fast > beta_slow >= 0 (BSA_ROPE_YARN)  */
-  double mscale;           /* > 0: multiplies every rotated element           */
+  double mscale;           /* > 0: multiplies every rotated element (a normal
+                              number in fp32)                                 */
   int heads_k;             /* heads of K; 0 = the plan's                      */
 } bsa_rope_config_t;
 
@@ -585,7 +586,8 @@ typedef struct bsa_cross_s* bsa_cross_t;
 
 /* bsa_cross_create — sizes of one cross attention.
  *   batch, n_q, n_kv >= 1; heads in [1, 256], a multiple of heads_kv >= 1;
- *   head_dim in {64, 128}; dtype; scale > 0, or 0 for 1 / sqrt(head_dim);
+ *   head_dim in {64, 128}; dtype; scale > 0 (with log2(e) scale a normal number
+ *   in fp32), or 0 for 1 / sqrt(head_dim);
  *   batch * heads * max(n_q, n_kv) below 2^31.
  * BSA_BF16 runs on the tensor cores (probabilities and their gradients are
  * rounded to bf16 as operands; every sum is fp32, its additions rounded toward
