@@ -609,7 +609,8 @@ class Rope:
         _check_view(q, self.q_shape, dt, dev, "q")
         if k is not None:
             _check_view(k, self.k_shape, dt, dev, "k")
-        if t_origin is not None and (t_origin.dtype != torch.int64 or t_origin.device != dev or
+        if t_origin is not None and (not isinstance(t_origin, torch.Tensor) or
+                                     t_origin.dtype != torch.int64 or t_origin.device != dev or
                                      t_origin.shape != self.q_shape[:1] or
                                      not t_origin.is_contiguous()):
             raise BsaError(1, f"t_origin must be an int64 tensor of shape {tuple(self.q_shape[:1])} on {dev}")
@@ -672,8 +673,8 @@ class CrossAttention:
     def _masks(self, kv_len, key_mask):
         for t, shape, types, name in ((kv_len, self.kv_shape[:1], (torch.int32,), "kv_len"),
                                       (key_mask, self.kv_shape[:2], (torch.bool, torch.uint8), "key_mask")):
-            if t is not None and (t.device != self.device or t.dtype not in types or
-                                  t.shape != shape or not t.is_contiguous()):
+            if t is not None and (not isinstance(t, torch.Tensor) or t.device != self.device or
+                                  t.dtype not in types or t.shape != shape or not t.is_contiguous()):
                 raise BsaError(1, f"{name} must be a contiguous {types[0]} tensor of shape "
                                   f"{tuple(shape)} on {self.device}")
         return (None if kv_len is None else kv_len.data_ptr(),
