@@ -5,10 +5,12 @@
 //   P  = exp(S - L),  dP = dO V^T,  D = rowsum(dO * O),  dS = P * (dP - D)
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
 // Products run on the tensor cores in tf32, three for one: with x = h + l, h the 11
-// leading bits that tf32 keeps, a b = ha hb + ha lb + la hb up to 2^-20 of its size
-// (la lb, and what tf32 drops of l), every sum in fp32.  As the tensor core rounds
-// each addition toward zero, a tile's products are summed from zero, the small ones
-// apart from the large, and joined to the running sum by fp32 additions.  The
+// leading bits that tf32 keeps, a b = ha hb + ha lb + la hb up to 1.75 2^-20 of its
+// size (la lb below 2^-20, and of each l the 2 of 13 bits that tf32 drops, 0.75 2^-21
+// for either; all short of the product, 0.27 2^-20 on average), every sum in fp32.
+// As the tensor core rounds each addition toward zero, a tile's products are summed
+// from zero, the small ones apart from the large, and joined to the running sum by
+// fp32 additions.  The
 // legacy warp MMA serves here: tcgen05 would want both parts of both operands in
 // shared memory, 256 KB for one pair of 128 x 128 tiles.  A warp owns 16 rows of
 // the result (query rows; keys for dK and dV) and keeps its logits, probabilities

@@ -55,7 +55,8 @@ __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2
 // One thread takes the same V elements (interleaved) or the same V pairs, V
 // elements at a time (half), of every head of a token, so that its angles are
 // formed once: the turn pos f / (2 pi) is reduced to [-1/2, 1/2] in double
-// (exact enough for positions of many millions) and only then goes to fp32.
+// (off by 4 2^-53 of itself: 2^-21 radians at position 2^30, where the range
+// ends) and only then goes to fp32.
 // Bound by memory: every element is read and written once, in V-element
 // accesses (16 bytes where the layout allows), consecutive threads on
 // consecutive parts of a token's head.  Measured on B200: HunyuanVideo's Q and

@@ -564,7 +564,8 @@ bsa_status bsa_rope_destroy(bsa_rope_t rope);
  *   q, q_out   [B, Ntot, heads, D] views
  *   k, k_out   [B, Ntot, heads_k, D] views (both NULL = Q alone)
  *   t_origin   device int64 [B] or NULL: added to t in each batch element (how
- *              far into its sequence it is); |t_origin + t| < 2^52
+ *              far into its sequence it is); |t_origin + t| <= 2^30 (an
+ *              angle is off by at most 2^-51 of itself)
  *   backward   0, or 1 for the transposed map: from gradients of the outputs
  *              to gradients of the inputs
  * An output may be the same view as its input (in place; the parts that are
@@ -593,8 +594,8 @@ typedef struct bsa_cross_s* bsa_cross_t;
  * rounded to bf16 as operands; every sum is fp32, its additions rounded toward
  * zero: a sum of one sign over 32 768 rows or keys loses about 2e-4, a tenth of
  * what its rounding to bf16 may cost).  BSA_F32 forms each product
- * as three of tf32 (within 2^-20 of its size) and sums in fp32; its inputs must
- * be finite where they are attended.
+ * as three of tf32 (short of its size by at most 2^-19, 0.3 2^-20 on average)
+ * and sums in fp32; its inputs must be finite where they are attended.
  * The object holds a status word on the current device; create it outside of
  * stream capture. */
 bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv,
