@@ -301,13 +301,23 @@ bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv, int 
     return fail(BSA_ERR_INVALID_ARG, "scale must be a normal number in fp32");
   if (dtype == BSA_BF16) plan_tc(&c);
   else plan_f32(&c);
-  // Gathering costs two launches and one more pass over K and V; with 2048 query
-  // rows or more to a K/V head that is less than the work on a masked key in ten.
+  // Gathering costs two launches (8 us together, 1 more per 1024 keys for the scan that
+  // numbers them) and a pass over K and V, whatever the mask; how many keys it saves only
+  // the device knows.  Forward, gathered against hidden, with 50% / 90% of the keys
+  // attended, us: bf16 32 760 queries x 512 keys x 12 heads 80 : 153 / 152 : 124, 2048 x
+  // 32 760 x 12 508 : 550 / 535 : 426, 2048 x 2048 x 1 33 : 24 / 33 : 25; fp32 2048 x 1100 x
+  // 12 171 : 304 / 279 : 304, 2048 x 32 760 x 1 419 : 631 / 625 : 630, 2048 x 300 x 1 30 : 23 /
+  // 31 : 25.  So it pays with many query rows and a mask that hides much, in fp32 at
+  // nearly every size, and costs up to 45 us with one K/V head of long keys that are
+  // mostly attended.
   c.gathers = (long long)(heads / heads_kv) * n_q >= 2048 && n_kv > 128;
   cudaError_t e = cudaGetDevice(&c.device);
   if (e != cudaSuccess) return cuda_fail(e);
   e = dtype == BSA_F32 ? bsa::prepare_cross_f32(head_dim) : bsa::prepare_cross_tc_forward(c.fwd, head_dim);
   if (e == cudaSuccess && dtype == BSA_BF16) e = bsa::prepare_cross_tc_backward(head_dim);
+  if (e == cudaErrorInvalidConfiguration)
+    return fail(BSA_ERR_CUDA, "a cross attention kernel was not compiled to the registers per thread that its register "
+                              "split assumes (kRegsLaunch): another compiler than the build's");
   if (e == cudaSuccess) e = cudaMalloc(&c.d_status, sizeof(int32_t));
   if (e != cudaSuccess) return cuda_fail(e);
   if ((e = cudaMemset(c.d_status, 0, sizeof(int32_t))) != cudaSuccess ||

@@ -330,6 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float m_use = m_run == -INFINITY ? 0.f : m_run;
         const float2 neg_m = make_float2(-m_use, -m_use);
+        // P is rounded to bf16, the type of V, as tcgen05 multiplies 16-bit operands of one
+        // type (tf32 for both would halve the rate and double V's bytes); the sum l takes
+        // P unrounded.
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[64];
 #pragma unroll

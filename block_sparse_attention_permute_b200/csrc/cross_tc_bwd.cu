@@ -2,6 +2,9 @@
 //
 // With S = Q K^T, P = exp(scale S - lse), dP = dO V^T, delta = rowsum(dO * O),
 // dS = P * (dP - delta):  dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO.
+// P and dS are rounded to bf16 as operands, the type of the tensors they multiply
+// (tcgen05 takes both operands in one 16-bit type); delta is read from the rounded O
+// where the keys fill more than one tile.  Together 0.3% of a gradient in norm.
 // Both kernels form S and dP anew (seven products in all where five would do):
 // dQ sums over keys and dK, dV over query rows, and with the sum in TMEM each
 // has a fixed order and needs no fp32 traffic through L2 or atomics.

@@ -523,7 +523,10 @@ typedef enum {
  *  NTK     theta -> theta * s^(d / (d - 2)) (d = 2: unchanged), which keeps the
  *          fastest pair and divides the slowest by s;
  *  YARN    (1 - g) f / s + g f with g the clamped ramp from 0 at beta_slow to 1
- *          at beta_fast turns within orig_len positions, orig_len f / (2 pi). */
+ *          at beta_fast turns within orig_len positions, orig_len f / (2 pi).
+ *          (Linear in the turns.  Code that ramps linearly in the pair's index i
+ *          between the pairs of beta_fast and beta_slow turns, with rounded ends,
+ *          gives the pairs between them other frequencies.) */
 typedef enum {
   BSA_ROPE_NONE = 0,
   BSA_ROPE_LINEAR = 1,
@@ -596,8 +599,8 @@ typedef struct bsa_cross_s* bsa_cross_t;
  * what its rounding to bf16 may cost).  BSA_F32 forms each product
  * as three of tf32 (short of its size by at most 2^-19, 0.3 2^-20 on average)
  * and sums in fp32; its inputs must be finite where they are attended.
- * The object holds a status word on the current device; create it outside of
- * stream capture. */
+ * The object holds a status word on the current device; create and destroy it
+ * outside of stream capture, and keep it while a graph with its calls is in use. */
 bsa_status bsa_cross_create(bsa_cross_t* out, int batch, int n_q, int n_kv,
                             int heads, int heads_kv, int head_dim,
                             bsa_dtype dtype, double scale);
