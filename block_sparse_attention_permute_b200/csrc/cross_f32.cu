@@ -21,11 +21,13 @@
 // touch all banks once.  Two or three CTAs of 64 rows (or keys) share an SM and cover
 // one another's loads and barriers.
 //
-// Measured on B200, 1560 rows x 226 keys x 12 heads of 128: forward 73 us, dQ 108 us,
-// dK and dV 113 us (23 to 38 TFLOP/s of fp32 products), a training step 318 us; packed
+// Measured on B200, 1560 rows x 226 keys x 12 heads of 128: forward 77 us, dQ 102 us,
+// dK and dV 125 us (28 to 35 TFLOP/s of fp32 products), a training step 319 us; packed
 // fp32 FMAs took 404 us (bound by 3.1 shared-memory wavefronts per 16-byte load), a
-// library's fp32 products with the rest in torch 387 us.  Bound by issue slots: nine
-// instructions for the three MMAs of a product, four of them the split.
+// library's fp32 products with the rest in torch 387 us.  Bound by the latency of
+// dependent instructions (load, split, MMA) with 7 or 8 warps on an SM: the tensor
+// pipe is 44 to 50% busy, issue slots 32 to 38%; and by 300 CTAs for 296 (dQ) or 444
+// (forward) places, and 288.
 #include "cross.cuh"
 
 namespace bsa {

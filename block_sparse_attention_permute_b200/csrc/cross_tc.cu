@@ -23,7 +23,7 @@
 // Measured on B200: 32 760 queries x 512 keys x 12 heads of 128 in 125 us (822
 // TFLOP/s, 0.51 of cuBLAS's burst rate) in a sustained loop, which runs at the
 // 1000 W cap and 1.7 GHz, 110 us in a short burst; tensor pipe 47% busy, MUFU 48%.
-// One query of 32 heads over 8 heads x 32 760 keys, batch 2: 45 us, 5.3 TB/s.
+// One query of 32 heads over 8 heads x 32 760 keys, batch 2: 45 to 47 us, 5.1 to 5.3 TB/s.
 // Bound by a stream's chain S -> softmax (1650 cycles, 1024 of them MUFU) -> PV
 // and by MMAs that read both operands from shared memory (84 cycles, not 64).  A
 // part of the exponentials as a polynomial on the FMA pipe did not pay (25%: 127.7

@@ -21,11 +21,11 @@
 // the next S.
 //
 // Measured on B200, 32 760 queries x 512 keys x 12 heads of 128 (a product is 51.5
-// GFLOP): row sums 36 us (203 MB, 5.6 TB/s), dQ 157 us (three products, 985
-// TFLOP/s), dK and dV 206 us (four, 1000 TFLOP/s), all at 1.5 GHz under the
-// profiler; 430 us together in a sustained loop at the 1000 W cap.  Tensor pipe 54%
-// busy in both: bound by the row work between two products (1600 cycles for P of a
-// tile, 600 for dS), beside which the other products run.
+// GFLOP): row sums 36 us (203 MB, 5.6 TB/s), dQ 147 us (three products, 1050
+// TFLOP/s), dK and dV 178 us (four, 1160 TFLOP/s), their reduction 10 us, each alone at
+// 1.8 to 1.9 GHz; 430 us together in a sustained loop at the 1000 W cap.  Tensor pipe
+// 52 and 56% busy: bound by the row work between two products (1600 cycles for P of
+// a tile, 600 for dS), beside which the other products run.
 #include "cross_tc.cuh"
 
 namespace bsa {
