@@ -34,6 +34,31 @@ def test_one_attended_key_among_many(n_q, n_kv, H, hkv, D, dtype, dev):  # noqa:
     assert dq[3].any() and dk[3].any()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_a_replayed_graph_counts_the_keys_anew(dtype, dev):  # noqa: F811
+    B, n_q, n_kv, H, D = 2, 130, 4500, 1, 64
+    op = bsa.CrossAttention(B, n_q, n_kv, H, H, D, dtype, device=dev)
+    x = [rand(s, dtype, dev, i) for i, s in enumerate((op.q_shape, op.kv_shape, op.kv_shape, op.q_shape))]
+    mask = torch.ones((B, n_kv), dtype=torch.bool, device=dev)
+    o, lse = op.forward(*x[:3], key_mask=mask, return_lse=True)
+    op.backward(x[3], *x[:3], o, lse, key_mask=mask)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = op.forward(*x[:3], key_mask=mask, return_lse=True)
+        dq, dk, dv = op.backward(x[3], *x[:3], o, lse, key_mask=mask)
+    for keys in ([4499], [0, 4499], [17], []):
+        mask.zero_()
+        mask[1, keys] = True
+        mask[0, 5:400] = True
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = oracle(*x, key_mask=mask)
+        for name, t in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+            check(name, t, ref[name])
+        assert bool(dq[1].any()) == bool(dk[1].any()) == (len(keys) > 1) and dq[0].any()
+
+
 @pytest.mark.parametrize("n_kv", [1, 40, 300])
 def test_a_single_key_that_is_nan_shows(n_kv, dev):  # noqa: F811
     # bf16 (fp32 asks for finite values at attended keys)
